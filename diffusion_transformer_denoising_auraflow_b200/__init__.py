@@ -102,6 +102,11 @@ _SIGS = {
     "af_quantize_rows_e4m3": [_P, _I, _I, _P, _P, _P],
     "af_ln_modulate_e4m3": [_P, _P, _P, _I, _P, _P, _I, _I, _I, _F, _P],
     "af_linear_fp8": [_P, _P, _P, _P, _P, _I, _I, _I, _P],
+    "af_quantize_rows_w4": [_P, _I, _I, _I, _I, _P, _P, _I, _P],
+    "af_dequantize_rows_w4": [_P, _P, _I, _I, _I, _I, _P, _I, _P],
+    "af_linear_w4": [_P, _I, _I, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _P],
+    "af_residual_norm": [_P, _P, _I, _F, _P, _P, _P, _I, _I, _P, _I, _P, _P, _P, _I, _I, _I, _F, _P],
+    "af_residual_norm_e4m3": [_P, _P, _I, _F, _P, _P, _P, _I, _I, _P, _I, _P, _P, _P, _P, _I, _I, _I, _F, _P],
     "af_status_string": [_I],
     "af_last_error": [],
 }
@@ -156,6 +161,7 @@ def _lens(t, n: int, name: str):
 
 AF_ERR_INVALID_ARG = 1
 AF_ERR_SHAPE = 2
+AF_ERR_UNSUPPORTED = 3
 AF_DTYPE_BF16 = 0
 AF_DTYPE_F32 = 1
 
@@ -670,6 +676,156 @@ def linear_fp8(A8, a_scale, W8, w_scale, C, stream=None):
     cp = c.dev(C, torch.bfloat16, "C")
     c.check()
     _check(lib.af_linear_fp8(ap, asp, wp, wsp, cp, M, N, K, _stream(stream)), where)
+
+
+# ---- 4-bit weights, and the residual between two norms
+
+_DTYPE_CODE = {torch.bfloat16: AF_DTYPE_BF16, torch.float32: AF_DTYPE_F32}
+
+
+def _either(t, name: str):
+    """The AF_DTYPE code of a tensor that may be bf16 or fp32."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPE_CODE:
+        raise TypeError(f"{name} must be a bfloat16 or float32 tensor")
+    return _DTYPE_CODE[t.dtype]
+
+
+def w4_shapes(N: int, K: int, group: int):
+    """Shapes of the codes (uint8) and scales (bfloat16) of an [N, K] weight in 4 bits."""
+    if group not in (32, 64, 128):
+        raise AFError(AF_ERR_UNSUPPORTED, "w4_shapes", f"group must be 32, 64 or 128, got {group}")
+    groups = (K + group - 1) // group
+    return (N, groups * group // 2), (groups, (N + 7) // 8 * 8)
+
+
+def _w4_args(c: _Call, codes, scales, N: int, K: int, group: int, where: str):
+    """Pointers and scale stride of a 4-bit weight: codes contiguous, scales
+    rows of at least N contiguous entries (a view of wider rows may be given)."""
+    want, (groups, _) = w4_shapes(N, K, group)
+    _need_shape(codes, want, "codes", where)
+    _need(scales.dim() == 2 and scales.shape[0] == groups and scales.shape[1] >= N, where,
+          f"scales must have shape ({groups}, >= {N}), got {tuple(scales.shape)}")
+    stride = scales.stride(0) if groups > 1 else max(scales.stride(0), (N + 7) // 8 * 8)
+    _need(scales.stride(1) == 1 or scales.shape[1] == 1, where, "scales must be contiguous along their rows")
+    if stride < N or stride % 8 != 0:
+        raise AFError(AF_ERR_UNSUPPORTED, where, f"the scales' row stride must be a multiple of 8 and at least {N}, "
+                                                 f"got {stride}")
+    cp = c.dev(codes, torch.uint8, "codes")
+    sp = c.rows(scales, torch.bfloat16, "scales", groups, stride, N)
+    for name, p in (("codes", cp), ("scales", sp)):
+        if (p.value or 0) % 16 != 0:
+            raise AFError(AF_ERR_UNSUPPORTED, where, f"{name} must start on a 16-byte boundary")
+    return cp, sp, stride
+
+
+def quantize_rows_w4(w, group: int, codes, scales, stream=None):
+    """4-bit codes and group scales of w [N, K] (bf16 or fp32) into codes and scales (shapes: w4_shapes)."""
+    where = "af_quantize_rows_w4"
+    N, K = w.shape
+    dt = _either(w, "w")
+    c = _Call(where)
+    cp, sp, stride = _w4_args(c, codes, scales, N, K, group, where)
+    wp = c.dev(w, w.dtype, "w")
+    c.check()
+    _check(lib.af_quantize_rows_w4(wp, dt, N, K, group, cp, sp, stride, _stream(stream)), where)
+
+
+def dequantize_rows_w4(codes, scales, group: int, out, stream=None):
+    """The values of 4-bit codes and scales into out [N, K] (bf16 or fp32)."""
+    where = "af_dequantize_rows_w4"
+    N, K = out.shape
+    dt = _either(out, "out")
+    c = _Call(where)
+    cp, sp, stride = _w4_args(c, codes, scales, N, K, group, where)
+    op = c.dev(out, out.dtype, "out")
+    c.check()
+    _check(lib.af_dequantize_rows_w4(cp, sp, stride, N, K, group, op, dt, _stream(stream)), where)
+
+
+def linear_w4(x, codes, scales, group: int, out, silu: bool = False, bias=None, stream=None):
+    """out [M, N] = f(x [M, K]) W^T + bias with W in 4 bits; f is SiLU or the
+    identity; x and out bf16 or fp32, bias fp32 [N] or None."""
+    where = "af_linear_w4"
+    M, K = x.shape
+    N = codes.shape[0]
+    _need_shape(out, (M, N), "out", where)
+    xt, ot = _either(x, "x"), _either(out, "out")
+    if bias is not None:
+        _need_shape(bias, (N,), "bias", where)
+    c = _Call(where)
+    cp, sp, stride = _w4_args(c, codes, scales, N, K, group, where)
+    xp, op = c.dev(x, x.dtype, "x"), c.dev(out, out.dtype, "out")
+    bp = c.dev(bias, torch.float32, "bias") if bias is not None else None
+    c.check()
+    _check(lib.af_linear_w4(xp, xt, 1 if silu else 0, cp, sp, stride, bp, op, ot, M, N, K, group, _stream(stream)),
+           where)
+
+
+NORMS = {"none": 0, "layer": 1, "rms": 2}
+
+
+def _residual_norm_args(c: _Call, where, x, branch, x_out, gate, shift, scale, mod_stride, residual_scale, post,
+                        post_weight, pre, pre_weight):
+    B, N, D = x.shape
+    dt = _either(x, "x")
+    if post not in NORMS or pre not in NORMS:
+        raise ValueError(f"post and pre must be one of {sorted(NORMS)}, got {post!r} and {pre!r}")
+    for name, t in (("branch", branch), ("x_out", x_out)):
+        if t is not None:
+            _need_shape(t, (B, N, D), name, where)
+    for name, t in (("post_weight", post_weight), ("pre_weight", pre_weight)):
+        if t is not None:
+            _need_shape(t, (D,), name, where)
+
+    def opt(t, dtype, name):
+        return None if t is None else c.dev(t, dtype, name)
+
+    def vec(t, name):
+        return None if t is None else c.rows(t, torch.float32, name, B, mod_stride, D)
+
+    for name, t in (("gate", gate), ("shift", shift), ("scale", scale)):
+        if t is not None and t.dim() > 0 and t.shape[-1] > 1:
+            _need(t.stride(-1) == 1, where, f"{name} must be contiguous along its last axis")
+    xp, bp, op = c.dev(x, x.dtype, "x"), opt(branch, x.dtype, "branch"), opt(x_out, x.dtype, "x_out")
+    return (xp, bp, dt, float(residual_scale), vec(gate, "gate"), vec(shift, "shift"), vec(scale, "scale"),
+            mod_stride, NORMS[post], opt(post_weight, torch.float32, "post_weight"), NORMS[pre],
+            opt(pre_weight, torch.float32, "pre_weight"), op)
+
+
+def residual_norm(x, branch, x_out, y, eps: float, gate=None, shift=None, scale=None, mod_stride: int = 0,
+                  residual_scale: float = 1.0, post: str = "none", post_weight=None, pre: str = "layer",
+                  pre_weight=None, stream=None):
+    """x' = x + residual_scale * gate * post(branch) * post_weight into x_out and
+    y = pre(x') * pre_weight * (1 + scale) + shift into y, in one pass over the
+    rows of x [B, N, D] (bf16 or fp32).  post and pre: "none", "layer" or "rms".
+    gate, shift, scale: fp32, sample b's vector at element b * mod_stride.
+    branch, x_out or y may be None (see af_residual_norm)."""
+    where = "af_residual_norm"
+    B, N, D = x.shape
+    if y is not None:
+        _need_shape(y, (B, N, D), "y", where)
+    c = _Call(where)
+    args = _residual_norm_args(c, where, x, branch, x_out, gate, shift, scale, int(mod_stride), residual_scale, post,
+                               post_weight, pre, pre_weight)
+    yp = None if y is None else c.dev(y, x.dtype, "y")
+    c.check()
+    _check(lib.af_residual_norm(*args, yp, B, N, D, float(eps), _stream(stream)), where)
+
+
+def residual_norm_e4m3(x, branch, x_out, y8, yscale, eps: float, gate=None, shift=None, scale=None,
+                       mod_stride: int = 0, residual_scale: float = 1.0, post: str = "none", post_weight=None,
+                       pre: str = "layer", pre_weight=None, stream=None):
+    """residual_norm with y as e4m3 codes y8 (uint8, B * N rows of D) and fp32 row scales yscale."""
+    where = "af_residual_norm_e4m3"
+    B, N, D = x.shape
+    _need(y8.numel() == B * N * D, where, f"y8 must hold {B * N * D} codes, got {y8.numel()}")
+    _need(yscale.numel() >= B * N, where, f"yscale must hold {B * N} values, got {yscale.numel()}")
+    c = _Call(where)
+    args = _residual_norm_args(c, where, x, branch, x_out, gate, shift, scale, int(mod_stride), residual_scale, post,
+                               post_weight, pre, pre_weight)
+    yp, sp = c.dev(y8, torch.uint8, "y8"), c.dev(yscale, torch.float32, "yscale")
+    c.check()
+    _check(lib.af_residual_norm_e4m3(*args, yp, sp, B, N, D, float(eps), _stream(stream)), where)
 
 
 AF_IPC_HANDLE_BYTES = 64

@@ -154,6 +154,42 @@ cudaError_t launch_init_normal(void* dst, bool f32, size_t numel, int cols, int 
 cudaError_t launch_convert_copy(const void* src, bool src_f32, void* dst, bool dst_f32, size_t numel, int cols,
                                 int interleave, cudaStream_t s);
 
+// Weights in 4 bits with group scales (w4.cu).  codes [N, ceil(K / group) *
+// group / 2], scales bf16 [ceil(K / group), scale_stride].
+struct W4Params {
+  const void* x;         // [M, K], bf16 or fp32 (x_f32)
+  const uint8_t* codes;
+  const uint16_t* scales;
+  const float* bias;     // [N] or nullptr
+  void* out;             // row m at out + m * out_stride, bf16 or fp32 (out_f32)
+  int M, N, K, group, scale_stride;
+  int64_t out_stride;
+  int x_f32, out_f32, silu;
+};
+cudaError_t launch_linear_w4(const W4Params& p, cudaStream_t s);
+cudaError_t launch_quantize_rows_w4(const void* w, bool f32, int N, int K, int group, uint8_t* codes,
+                                    uint16_t* scales, int scale_stride, cudaStream_t s);
+cudaError_t launch_dequantize_rows_w4(const uint8_t* codes, const uint16_t* scales, int scale_stride, int N, int K,
+                                      int group, void* out, bool f32, cudaStream_t s);
+
+// Gated residual between two norms (residual_norm.cu).
+enum NormKind : int { NORM_NONE = 0, NORM_LAYER = 1, NORM_RMS = 2 };
+struct ResidualNormParams {
+  const void* x;             // [B, rows_per_batch, D], bf16 or fp32 like branch, x_out and y
+  const void* branch;        // nullptr: x' = x
+  void* x_out;               // nullptr: x' is not stored; may be x
+  void* y;                   // nullptr: no second norm; e4m3 codes when yscale != nullptr
+  float* yscale;             // [B * rows_per_batch]
+  const float* gate;         // of sample b at + b * mod_stride; nullptr: 1
+  const float* shift;        // nullptr: 0
+  const float* scale;        // nullptr: 0
+  const float* post_weight;  // [D]; nullptr: 1
+  const float* pre_weight;   // [D]; nullptr: 1
+  int mod_stride, post, pre, B, rows_per_batch, D;
+  float residual_scale, eps;
+};
+cudaError_t launch_residual_norm(const ResidualNormParams& p, bool f32, cudaStream_t s);
+
 // The fp32 forward's kernels (fp32.cu).  mode: EPI_STORE (rows remapped per
 // sample) or EPI_GATE_RES (out[m, n] += gate[b, n] * acc).
 cudaError_t f32_gemm(const float* A, const float* W, int M, int N, int K, int mode, float* out, int ldo,

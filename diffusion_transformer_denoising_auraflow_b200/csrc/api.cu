@@ -1703,6 +1703,77 @@ af_status af_linear_fp8(const uint8_t* A, const float* a_scale, const uint8_t* W
   return AF_OK;
 }
 
+static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// The layout rules of 4-bit weights that every call taking them shares.
+static af_status check_w4(const void* codes, const void* scales, int scale_stride, int N, int K, int group) {
+  if (!codes || !scales || N <= 0 || K <= 0 || scale_stride < N) return AF_ERR_INVALID_ARG;
+  if (!(group == 32 || group == 64 || group == 128) || K > 65536) return AF_ERR_UNSUPPORTED;
+  if (!aligned16(codes) || !aligned16(scales) || scale_stride % 8 != 0) return AF_ERR_UNSUPPORTED;
+  return AF_OK;
+}
+
+static bool is_dtype(int t) { return t == AF_DTYPE_BF16 || t == AF_DTYPE_F32; }
+
+af_status af_quantize_rows_w4(const void* w, int w_dtype, int N, int K, int group, uint8_t* codes, uint16_t* scales,
+                              int scale_stride, void* stream) {
+  if (!w || !is_dtype(w_dtype)) return AF_ERR_INVALID_ARG;
+  AF_TRY(check_w4(codes, scales, scale_stride, N, K, group));
+  AF_CUDA(launch_quantize_rows_w4(w, w_dtype == AF_DTYPE_F32, N, K, group, codes, scales, scale_stride,
+                                  static_cast<cudaStream_t>(stream)));
+  return AF_OK;
+}
+
+af_status af_dequantize_rows_w4(const uint8_t* codes, const uint16_t* scales, int scale_stride, int N, int K,
+                                int group, void* out, int out_dtype, void* stream) {
+  if (!out || !is_dtype(out_dtype)) return AF_ERR_INVALID_ARG;
+  AF_TRY(check_w4(codes, scales, scale_stride, N, K, group));
+  AF_CUDA(launch_dequantize_rows_w4(codes, scales, scale_stride, N, K, group, out, out_dtype == AF_DTYPE_F32,
+                                    static_cast<cudaStream_t>(stream)));
+  return AF_OK;
+}
+
+af_status af_linear_w4(const void* x, int x_dtype, int silu, const uint8_t* codes, const uint16_t* scales,
+                       int scale_stride, const float* bias, void* out, int out_dtype, int M, int N, int K, int group,
+                       void* stream) {
+  if (!x || !out || M <= 0 || !is_dtype(x_dtype) || !is_dtype(out_dtype)) return AF_ERR_INVALID_ARG;
+  AF_TRY(check_w4(codes, scales, scale_stride, N, K, group));
+  const W4Params p{x, codes, scales, bias, out, M, N, K, group, scale_stride, N, x_dtype == AF_DTYPE_F32,
+                   out_dtype == AF_DTYPE_F32, silu != 0};
+  AF_CUDA(launch_linear_w4(p, static_cast<cudaStream_t>(stream)));
+  return AF_OK;
+}
+
+static af_status residual_norm_call(ResidualNormParams p, int dtype, int N, void* stream) {
+  if (!p.x || (!p.x_out && !p.y) || !is_dtype(dtype)) return AF_ERR_INVALID_ARG;
+  if (p.B <= 0 || N <= 0 || p.D <= 0 || p.mod_stride < 0 || !(p.eps >= 0.f)) return AF_ERR_INVALID_ARG;
+  if (p.post < NORM_NONE || p.post > NORM_RMS || p.pre < NORM_NONE || p.pre > NORM_RMS) return AF_ERR_INVALID_ARG;
+  if (!p.branch && (p.gate || p.post_weight || p.post != NORM_NONE)) return AF_ERR_INVALID_ARG;
+  if (!p.y && (p.shift || p.scale || p.pre_weight)) return AF_ERR_INVALID_ARG;
+  if (p.D > 16384 || static_cast<int64_t>(p.B) * N > INT32_MAX) return AF_ERR_UNSUPPORTED;
+  AF_CUDA(launch_residual_norm(p, dtype == AF_DTYPE_F32, static_cast<cudaStream_t>(stream)));
+  return AF_OK;
+}
+
+af_status af_residual_norm(const void* x, const void* branch, int dtype, float residual_scale, const float* gate,
+                           const float* shift, const float* scale, int mod_stride, int post, const float* post_weight,
+                           int pre, const float* pre_weight, void* x_out, void* y, int B, int N, int D, float eps,
+                           void* stream) {
+  const ResidualNormParams p{x,           branch,     x_out,      y,    nullptr, gate, shift, scale,         post_weight,
+                             pre_weight,  mod_stride, post,       pre,  B,       N,    D,     residual_scale, eps};
+  return residual_norm_call(p, dtype, N, stream);
+}
+
+af_status af_residual_norm_e4m3(const void* x, const void* branch, int dtype, float residual_scale, const float* gate,
+                                const float* shift, const float* scale, int mod_stride, int post,
+                                const float* post_weight, int pre, const float* pre_weight, void* x_out, uint8_t* y8,
+                                float* yscale, int B, int N, int D, float eps, void* stream) {
+  if (!y8 || !yscale) return AF_ERR_INVALID_ARG;
+  const ResidualNormParams p{x,           branch,     x_out,      y8,   yscale,  gate, shift, scale,         post_weight,
+                             pre_weight,  mod_stride, post,       pre,  B,       N,    D,     residual_scale, eps};
+  return residual_norm_call(p, dtype, N, stream);
+}
+
 // A plain bf16 product C[M, N] = A W^T as GEMM parameters.
 static GemmParams plain_gemm(uint16_t* C, int M, int N, int K) {
   GemmParams p;

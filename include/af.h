@@ -378,6 +378,46 @@ af_status af_ln_modulate_e4m3(const uint16_t* x, const float* shift, const float
 af_status af_linear_fp8(const uint8_t* A, const float* a_scale, const uint8_t* W, const float* w_scale, uint16_t* C,
                         int M, int N, int K, void* stream);
 
+/* ---- 4-bit weights ----------------------------------------------------------
+ * A weight matrix [N, K] in 4 bits with one bf16 scale per row and group of
+ * `group` columns (32, 64 or 128):
+ *   value(n, k) = scale(k / group, n) * (code(n, k) - 8),   code in 0..15.
+ *   codes:  device uint8 [N, ceil(K / group) * group / 2], code k of row n in
+ *           the low (k even) or high (k odd) nibble of byte k / 2; codes
+ *           behind column K are 8.
+ *   scales: device bf16 [ceil(K / group), scale_stride], scale_stride >= N;
+ *           entries at and behind column N are neither read into a result
+ *           nor written.
+ * codes and scales start on 16-byte boundaries, scale_stride is a multiple
+ * of 8 and K at most 65536 (else AF_ERR_UNSUPPORTED); so a range of rows of a
+ * larger matrix that starts at a multiple of 8 is a matrix of its own (codes +
+ * first * row bytes, scales + first, the same scale_stride).  w, x, out and
+ * bias need no alignment beyond their type's.  Dtypes are AF_DTYPE_BF16 or
+ * AF_DTYPE_F32.  The pipeline guide's 4-bit loading ([PIPE] bitsandbytes
+ * sections) fixes no format; this is the framework's own. */
+
+/* Codes and scales of w (device [N, K]).  Per row and group, with a = max |w|
+ * over the group: scale = a / 7 rounded to bf16 (nearest even), code = 8 + the
+ * whole number nearest to w / scale (ties to even), held to 0..15; 8 where
+ * the scale is zero.  Values must be finite. */
+af_status af_quantize_rows_w4(const void* w, int w_dtype, int N, int K, int group, uint8_t* codes, uint16_t* scales,
+                              int scale_stride, void* stream);
+
+/* The values that codes and scales stand for: out device [N, K] (bf16 rounds
+ * to nearest even, fp32 is exact). */
+af_status af_dequantize_rows_w4(const uint8_t* codes, const uint16_t* scales, int scale_stride, int N, int K,
+                                int group, void* out, int out_dtype, void* stream);
+
+/* out[m, n] = bias[n] + sum_k f(x[m, k]) value(n, k), f = SiLU if silu != 0,
+ * else the identity: the adaLN-Zero modulations W silu(temb) ([ARCH]
+ * §联合注意力块) and other projections of a few rows.  x (and silu(x)) enter
+ * unrounded, sums are kept in fp32.
+ *   x: device [M, K]; out: device [M, N]; bias: device float [N] or NULL.
+ * out must not overlap the inputs. */
+af_status af_linear_w4(const void* x, int x_dtype, int silu, const uint8_t* codes, const uint16_t* scales,
+                       int scale_stride, const float* bias, void* out, int out_dtype, int M, int N, int K, int group,
+                       void* stream);
+
 /* Host-side sigma schedule of the flow-match Euler sampler ([DEEP] §2.3:
  * num_train_timesteps 1000, shift 1.73, 25 steps): n_steps + 1 values
  * sigma_i = k s_i / (1 + (k - 1) s_i) with s = linspace(1, 1/num_train,
@@ -422,6 +462,42 @@ af_status af_profile_end(af_scratch* s, void* stream, double ms[AF_NUM_KERNEL_CL
  *   at shift[b * mod_stride + d]. */
 af_status af_ln_modulate(const uint16_t* x, const float* shift, const float* scale, int mod_stride,
                          uint16_t* y, int B, int N, int D, float eps, void* stream);
+
+/* Norms after and before a sub-block fused with the gated, scaled residual
+ * between them:
+ *   u  = post(branch) * post_weight
+ *   x' = x + residual_scale * gate[b] * u                       -> x_out
+ *   y  = pre(x') * pre_weight * (1 + scale[b]) + shift[b]       -> y
+ * post, pre: AF_NORM_NONE, AF_NORM_LAYER (FP32 LayerNorm without affine
+ * weights, as af_ln_modulate) or AF_NORM_RMS (v / sqrt(mean(v^2) + eps)).
+ * With post = NONE, pre = LAYER it is the step between the two halves of an
+ * adaLN-Zero block ([ARCH] §调制与归一化); with pre = NONE the pre-final
+ * modulation.  Statistics in fp32; y is formed from x' before x' is rounded
+ * to its type.
+ *   x, branch, x_out, y: device [B*N, D], all bf16 or all fp32 (dtype).
+ *   gate, shift, scale: device float, element (b, d) at b * mod_stride + d
+ *   (mod_stride 0: one vector for all samples); post_weight, pre_weight:
+ *   device float [D].
+ * Each may be NULL: branch (then x' = x and gate, post_weight must be NULL,
+ * post NONE), gate, post_weight, pre_weight (1), shift, scale (0), x_out (x'
+ * is not stored), y (no second norm; shift, scale, pre_weight must be NULL),
+ * but not both x_out and y.  x_out may be x and y may be branch or x; no
+ * other overlap.  D at most 16384 (else AF_ERR_UNSUPPORTED). */
+#define AF_NORM_NONE 0
+#define AF_NORM_LAYER 1
+#define AF_NORM_RMS 2
+af_status af_residual_norm(const void* x, const void* branch, int dtype, float residual_scale, const float* gate,
+                           const float* shift, const float* scale, int mod_stride, int post, const float* post_weight,
+                           int pre, const float* pre_weight, void* x_out, void* y, int B, int N, int D, float eps,
+                           void* stream);
+
+/* The same with y as e4m3 codes y8 (device uint8 [B*N, D]) and row scales
+ * yscale (device float [B*N]), with the rule of af_quantize_rows_e4m3 applied
+ * to the fp32 y: the input of af_linear_fp8. */
+af_status af_residual_norm_e4m3(const void* x, const void* branch, int dtype, float residual_scale, const float* gate,
+                                const float* shift, const float* scale, int mod_stride, int post,
+                                const float* post_weight, int pre, const float* pre_weight, void* x_out, uint8_t* y8,
+                                float* yscale, int B, int N, int D, float eps, void* stream);
 
 /* C = A W^T on the tcgen05 tensor cores, bf16 in, fp32 accumulate, bf16 out.
  *   A: device bf16[M, K]; W: device bf16[N, K]; C: device bf16[M, N].

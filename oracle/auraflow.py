@@ -736,3 +736,66 @@ def rel_l2(a, b) -> float:
     """||a - b||_2 / ||b||_2 in fp64 (b is the reference)."""
     a, b = _f(a), _f(b)
     return float(np.linalg.norm((a - b).ravel()) / max(np.linalg.norm(b.ravel()), 1e-300))
+
+
+# --------------------------------------------------------------------------
+# 4-bit weights with group scales, and the residual between two norms
+# (extensions next to the 8-bit variant and the adaLN modulate above)
+# --------------------------------------------------------------------------
+
+def quantize_rows_w4(w, group: int):
+    """Codes [N, ceil(K / group) * group] in 0..15 (8 behind column K) and
+    scales [ceil(K / group), N]: a = max |w| per row and group, scale = a / 7
+    rounded to bf16, code = 8 + the whole number nearest to w / scale (ties
+    to even), held to 0..15; 8 where the scale is zero."""
+    w = _f(w)
+    n, k = w.shape
+    groups = -(-k // group)
+    wp = np.zeros((n, groups * group))
+    wp[:, :k] = w
+    wp = wp.reshape(n, groups, group)
+    s = round_bf16(np.max(np.abs(wp), axis=2) / 7.0)
+    q = np.where(s[:, :, None] > 0, np.rint(wp / np.where(s > 0, s, 1.0)[:, :, None]), 0.0)
+    return np.clip(q + 8, 0, 15).astype(np.uint8).reshape(n, groups * group), s.T
+
+
+def dequantize_rows_w4(codes, scales, group: int, k: int):
+    """scale * (code - 8), [N, K]."""
+    return ((_f(codes) - 8.0) * np.repeat(_f(scales).T, group, axis=1))[:, :k]
+
+
+def linear_w4(x, codes, scales, group: int, silu_in: bool = False, bias=None):
+    """f(x) W^T + bias with W = dequantize_rows_w4."""
+    x = silu(x) if silu_in else _f(x)
+    out = x @ dequantize_rows_w4(codes, scales, group, x.shape[1]).T
+    return out if bias is None else out + _f(bias)
+
+
+def norm(v, kind: str, eps: float):
+    """"none", "layer" (layer_norm above) or "rms": v / sqrt(mean(v^2) + eps)."""
+    if kind == "layer":
+        return layer_norm(v, eps)
+    v = _f(v)
+    return v if kind == "none" else v / np.sqrt(np.mean(v * v, axis=-1, keepdims=True) + eps)
+
+
+def residual_norm(x, branch, eps, gate=None, shift=None, scale=None, residual_scale=1.0, post="none",
+                  post_weight=None, pre="layer", pre_weight=None):
+    """(x', y): x' = x + residual_scale gate post(branch) post_weight,
+    y = pre(x') pre_weight (1 + scale) + shift; gate, shift, scale [B, D]."""
+    x = _f(x)
+    if branch is not None:
+        u = norm(branch, post, eps)
+        if post_weight is not None:
+            u = u * _f(post_weight)
+        if gate is not None:
+            u = u * _f(gate)[:, None, :]
+        x = x + residual_scale * u
+    y = norm(x, pre, eps)
+    if pre_weight is not None:
+        y = y * _f(pre_weight)
+    if scale is not None:
+        y = y * (1.0 + _f(scale)[:, None, :])
+    if shift is not None:
+        y = y + _f(shift)[:, None, :]
+    return x, y

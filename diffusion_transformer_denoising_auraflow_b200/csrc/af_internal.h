@@ -57,7 +57,7 @@ constexpr int GEMM_RES_BYTES = 4 * 2 * 32 * 32 * 2;
 constexpr int GEMM_SMEM_BYTES =
     GEMM_STAGES * (GEMM_BM + GEMM_BN) * GEMM_BK * 2 + GEMM_RES_BYTES + 1024 /*barriers*/ + 1024 /*align*/;
 
-// Host helpers (gemm.cu)
+// Host helpers (gemm.cu); swizzle_bytes 128, 64 or 0 (none)
 bool encode_tmap_2d(CUtensorMap* map, const void* ptr, uint64_t inner, uint64_t outer, uint64_t row_bytes,
                     uint32_t box_inner, uint32_t box_outer, bool bytes = false, int swizzle_bytes = 128);
 bool encode_tmap_3d(CUtensorMap* map, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1_bytes,
@@ -165,6 +165,7 @@ struct W4Params {
   int M, N, K, group, scale_stride;
   int64_t out_stride;
   int x_f32, out_f32, silu;
+  int* err = nullptr;    // device error word
 };
 cudaError_t launch_linear_w4(const W4Params& p, cudaStream_t s);
 cudaError_t launch_quantize_rows_w4(const void* w, bool f32, int N, int K, int group, uint8_t* codes,

@@ -1708,7 +1708,8 @@ static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 // The layout rules of 4-bit weights that every call taking them shares.
 static af_status check_w4(const void* codes, const void* scales, int scale_stride, int N, int K, int group) {
   if (!codes || !scales || N <= 0 || K <= 0 || scale_stride < N) return AF_ERR_INVALID_ARG;
-  if (!(group == 32 || group == 64 || group == 128) || K > 65536) return AF_ERR_UNSUPPORTED;
+  if (!(group == 32 || group == 64 || group == 128) || K > 65536 || N > (1 << 30))
+    return AF_ERR_UNSUPPORTED;
   if (!aligned16(codes) || !aligned16(scales) || scale_stride % 8 != 0) return AF_ERR_UNSUPPORTED;
   return AF_OK;
 }

@@ -389,7 +389,7 @@ af_status af_linear_fp8(const uint8_t* A, const float* a_scale, const uint8_t* W
  *           entries at and behind column N are neither read into a result
  *           nor written.
  * codes and scales start on 16-byte boundaries, scale_stride is a multiple
- * of 8 and K at most 65536 (else AF_ERR_UNSUPPORTED); so a range of rows of a
+ * of 8, K at most 65536 and N at most 2^30 (else AF_ERR_UNSUPPORTED); so a range of rows of a
  * larger matrix that starts at a multiple of 8 is a matrix of its own (codes +
  * first * row bytes, scales + first, the same scale_stride).  w, x, out and
  * bias need no alignment beyond their type's.  Dtypes are AF_DTYPE_BF16 or

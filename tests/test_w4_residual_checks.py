@@ -92,6 +92,7 @@ def test_linear_w4_entry_refuses():
     assert _lin(ss=12) == UNSUPPORTED               # not a multiple of 8
     assert _lin(codes=P + 8) == UNSUPPORTED and _lin(scales=P + 2) == UNSUPPORTED
     assert _lin(K=65537) == UNSUPPORTED
+    assert _lin(N=(1 << 30) + 8, ss=(1 << 30) + 8) == UNSUPPORTED
 
 
 def test_quantize_entries_refuse():

@@ -107,271 +107,433 @@ cudaError_t launch_dequantize_rows_w4(const uint8_t* codes, const uint16_t* scal
 // ------------------------------------------------------------------ product
 // out[m, n] = bias[n] + sum_k f(x[m, k]) s[k / G, n] (c[n, k] - 8).
 //
-// Each group's sum of f(x) (c - 8) runs on mma.sync m16n8k16: the weights are
-// the 16-row operand, as the whole numbers c - 8, exact in bf16; the columns
-// are rows of x.  bf16 x is one column; fp32 x (and SiLU of either) is cut
-// into three bf16 pieces of 8 bits each that add up to it exactly, three
-// columns, so with the eight columns an instruction has anyway one or two
-// fp32 rows cost what one bf16 row does.  Products are exact, sums fp32, and
-// a group's sum is multiplied by its fp32 scale once.
+// Each group's sum runs on mma.sync m16n8k32 in whole numbers: the weights are
+// the 16-row operand, the codes c as they are (two masks and a shift unpack
+// eight), the columns are rows of x as 24-bit fixed point, cut into three
+// signed bytes, a column each.  One factor per row of x and 256 columns takes
+// the largest magnitude a there to +-8355000, so a value is off by at most
+// a 2^-24, half an fp32 step of a.  Sums are exact (at most 15 * 128 * 128);
+// sum c q - 8 sum q is formed with 8 sum q known per group and column, then
+// multiplied by the group's scale and added up in fp32.
+// Other operands cost more to make: c - 8 in fp16 (x in two pieces) took 77
+// instructions per 16 rows and 64 columns against 50, near the 91 issue slots
+// that HBM leaves time for; 743424 x 3072 with two rows of x took 218 us
+// against 188-197.
+// A row of x that holds an infinity or NaN has no fixed point: its results are
+// summed value by value in fp32 (w4_plain_sum).
 //
-// Bound: the code bytes from HBM (4.25 bits a weight at G = 64).  A 512-thread
-// CTA per SM streams them with a TMA producer warp through a ring of 32 KB
-// stages; 16 consumer warps are RW x KW: RW blocks of 16 rows by KW chunks of
-// 256 columns (128 bytes of codes).  Rows of a stage are 128-byte lines under
-// the 128-byte swizzle, so the fragment reads (lane (g, t): 4 bytes = 8 codes
-// of row g, word t of a 16-byte piece) touch all 32 banks.  Of a word the
-// codes p and p + 4 form one operand register; x lies in shared memory in
-// that order (0, 4, 1, 5, 2, 6, 3, 7 of every eight).
+// Bound: the code bytes from HBM (4.25 bits a weight at G = 64).  One CTA of W
+// warps per SM, RW x KW of them: RW blocks of 32 rows by KW ways to
+// share the columns, in chunks of 256 (128 bytes of codes).  Each warp streams
+// its own 32 rows through its own ring of 4 KB stages: one lane issues the TMA
+// loads of a stage as soon as the warp has read it, so no warp waits for
+// another until a tile's sums are joined.  Rows of a stage are 128-byte lines
+// under the 128-byte swizzle.  A lane (g, t) holds an equal share of a row's
+// group (4, 8 or 16 bytes at G = 32, 64, 128), read by one load; the rows are
+// dealt to g = 0..7 so that each load touches all 32 banks.  Of a word of
+// eight codes, p and p + 4 form one operand register; x lies in shared memory
+// in the order in which the lanes need it.
 constexpr int W4_WARPS = 16;
-constexpr int W4_THREADS = 32 * (W4_WARPS + 1);
+constexpr int W4_THREADS = 32 * W4_WARPS;
+// Rows per warp by the 8-column blocks of x: 32 share the reads of x, with
+// more blocks than one 16 leave registers for four warps per scheduler.
+__host__ __device__ constexpr int w4_rows(int nt) { return nt == 1 ? 32 : 16; }
 constexpr int W4_CHUNK = 256;                             // columns per chunk
-constexpr int W4_STAGE = W4_WARPS * 16 * W4_CHUNK / 2;    // code bytes per stage
-constexpr int W4_RED_LD = 20;                             // floats between columns of a warp's sums: no bank conflicts
 constexpr int W4_MAX_NT = 4;                              // 8-column blocks
 constexpr int W4_SMEM_MAX = 227 * 1024;
-constexpr int W4_MAX_STAGES = 8;
+constexpr int W4_MAX_STAGES = 4;
+constexpr int W4_MAX_ROWS = W4_MAX_NT * 8 / 3;            // rows of x per CTA, three columns each
 
 struct W4Launch {
   W4Params p;
-  int m0, rows_m, parts;    // this launch's rows of x and pieces (columns) of each
-  int rw;                   // row blocks of 16 per CTA tile; W4_WARPS / rw chunks per stage
+  int rows_m;               // rows of x per CTA (blockIdx.y: which)
+  int rw;                   // row blocks per CTA tile; the other warps share a block's chunks
   int tiles, chunks, seg_chunks, segs, stages;
   int x_pitch;              // bytes between columns of x in shared memory
+  int x_vec;                // x in 16-byte loads: aligned, K a multiple of 8
 };
+
+constexpr float W4_FIX = 8355000.0f;       // largest fixed-point value; three signed bytes reach 8355711
+constexpr float W4_TINY = 0x1p-104f;       // a row's chunk below this counts in steps of W4_TINY / W4_FIX
+constexpr float W4_MAGIC = 12582912.0f;    // 1.5 * 2^23: the bits of W4_MAGIC + i are its bits + i for |i| < 2^22
+constexpr int W4_MAGIC_BITS = 0x4B400000;
 
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
+__device__ __forceinline__ uint64_t lds_u64(uint32_t a) {
+  uint64_t v;
+  asm volatile("ld.shared.u64 %0, [%1];" : "=l"(v) : "r"(a));
+  return v;
+}
+// packed fp32 pairs
+__device__ __forceinline__ uint64_t w4_pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t w4_add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t w4_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ void sts_f1(uint32_t a, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
 __device__ __forceinline__ float lds_bf16(uint32_t a) {
   uint16_t v;
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
   return w4_bf16(v);
 }
-// two codes of a word, c in the low and high half, as bf16 c - 8: 128 + c is
-// the pattern 0x4300 | c, and the difference to 136 is exact
-__device__ __forceinline__ uint32_t w4_pair(uint32_t w) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, 0x000F000F, 0x43004300, 0xEA;" : "=r"(r) : "r"(w));  // (a & b) | c
-  asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(r) : "r"(0x43084308u));
-  return r;
-}
-__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                          uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// d = a b + c: 16 rows of codes (unsigned bytes), 8 columns of x (signed), 32 deep.
+__device__ __forceinline__ void mma_16832(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1, int c0, int c1, int c2, int c3) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+      : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(c0), "r"(c1), "r"(c2), "r"(c3));
 }
 
-// Columns [k0, k0 + n) of this launch's rows of x (zero behind column K) into
-// shared memory.  A thread takes eight columns of a row: one 16-byte store
-// per piece.  Each piece is the value's leading 8 bits, truncated; the last
-// is what remains.  Infinities and NaN stay whole in the first piece.
-__device__ __forceinline__ void w4_stage_x(const W4Launch& L, uint32_t xs, int k0, int n) {
+// sum_k f(x[m, k]) value(n, k) term by term, for rows of x that are not finite.
+__device__ __noinline__ float w4_plain_sum(const W4Params& p, int m, int n) {
+  const uint8_t* cr = p.codes + static_cast<size_t>(n) * ((p.K + p.group - 1) / p.group) * (p.group / 2);
+  float v = 0.f;
+  for (int k = 0; k < p.K; ++k) {
+    const int c = (cr[k >> 1] >> (4 * (k & 1))) & 15;
+    float x = w4_load(p.x, p.x_f32, static_cast<size_t>(m) * p.K + k);
+    if (p.silu) x = w4_silu(x);
+    v += x * (w4_bf16(p.scales[static_cast<size_t>(k / p.group) * p.scale_stride + n]) * (c - 8));
+  }
+  return v;
+}
+
+// Where x lies in shared memory, as addresses: `cols` columns of bytes, the
+// chunks' factors [chunk][NT * 8] and the groups' offsets [group][NT * 8].
+struct W4X {
+  uint32_t x, fac, off;
+};
+
+// `chunks` chunks of this CTA's rows of x from column k0 (zero behind column K)
+// into shared memory.  A warp takes a row's chunk, a lane eight columns: of
+// each digit one 8-byte store in the order 0, 2, 4, 6, 1, 3, 5, 7, as a word of
+// codes unpacks.  fac: what the chunk's sums of a digit stand for; off: minus
+// the magic number and 8 sum q of each group.  bad[m] is set if a value is not finite.
+template <int G, int NT>
+__device__ __forceinline__ void w4_stage_x(const W4Launch& L, int m0, int rows, const W4X& X, int* bad, int k0,
+                                           int chunks) {
   const W4Params& p = L.p;
-  const int per = n / 8;
-  for (int i = threadIdx.x; i < L.rows_m * per; i += 32 * W4_WARPS) {
-    const int m = i / per, j = 8 * (i - m * per);
-    float v[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int U = 2;  // chunks per warp whose loads are in flight together
+  const int items = rows * chunks;
+  for (int i0 = warp; i0 < items; i0 += U * W4_WARPS) {
+    uint4 raw[U][2];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int k = k0 + j + e;
-      v[e] = k < p.K ? w4_load(p.x, p.x_f32, static_cast<size_t>(L.m0 + m) * p.K + k) : 0.f;
-      if (p.silu) v[e] = w4_silu(v[e]);
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * W4_WARPS;
+      raw[u][0] = raw[u][1] = make_uint4(0, 0, 0, 0);
+      if (i >= items) continue;
+      const int m = i / chunks, k = k0 + 8 * ((i - m * chunks) * 32 + lane);
+      const size_t at = static_cast<size_t>(m0 + m) * p.K + k;
+      if (L.x_vec && k + 8 <= p.K) {
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.x) + at * (p.x_f32 ? 4 : 2));
+        raw[u][0] = src[0];
+        if (p.x_f32) raw[u][1] = src[1];
+      } else if (p.x_f32) {
+        const uint32_t* src = static_cast<const uint32_t*>(p.x) + at;
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = k + e < p.K ? src[e] : 0u;
+        raw[u][0] = make_uint4(w[0], w[1], w[2], w[3]);
+        raw[u][1] = make_uint4(w[4], w[5], w[6], w[7]);
+      } else {
+        const uint16_t* src = static_cast<const uint16_t*>(p.x) + at;
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = k + e < p.K ? src[e] : 0u;
+        raw[u][0] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+      }
     }
-    const uint32_t dst = xs + m * L.parts * L.x_pitch + 2 * j;
-    for (int part = 0; part < L.parts; ++part) {
-      uint32_t h[8];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * W4_WARPS;
+      if (i >= items) break;
+      const int m = i / chunks, c = i - m * chunks;
+      const uint32_t q[8] = {raw[u][0].x, raw[u][0].y, raw[u][0].z, raw[u][0].w,
+                             raw[u][1].x, raw[u][1].y, raw[u][1].z, raw[u][1].w};
+      float v[8], a = W4_TINY;
+      bool fine = true;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        h[e] = __float_as_uint(v[e]) & 0xFFFF0000u;
-        const float hv = __uint_as_float(h[e]);
-        if (L.parts > 1 && (h[e] & 0x7F800000u) == 0x7F800000u) {
-          if (v[e] != v[e]) h[e] = 0x7FC00000u;  // a NaN may have its payload in the bits cut off
-          v[e] = 0.f;
-        } else {
-          v[e] -= hv;
-        }
+        v[e] = p.x_f32 ? __uint_as_float(q[e]) : (e & 1) ? bf16_hi(q[e / 2]) : bf16_lo(q[e / 2]);
+        if (p.silu) v[e] = w4_silu(v[e]);
+        a = fmaxf(a, fabsf(v[e]));
+        fine &= fabsf(v[e]) < INFINITY;
       }
-      sts128(dst + part * L.x_pitch, make_uint4((h[0] >> 16) | h[4], (h[1] >> 16) | h[5], (h[2] >> 16) | h[6],
-                                                (h[3] >> 16) | h[7]));
+      asm volatile("redux.sync.max.abs.f32 %0, %0, 0xffffffff;" : "+f"(a));
+      if (!fine) bad[m] = 1;
+      const float up = __fdiv_rn(W4_FIX, a);
+      uint32_t f[8];  // three signed bytes each: q = d0 + 256 d1 + 65536 d2
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        f[e] = (static_cast<uint32_t>(__float2int_rn(fminf(fmaxf(v[e] * up, -W4_FIX), W4_FIX))) + 0x808080u) ^ 0x808080u;
+#pragma unroll
+      for (int d = 0; d < 3; ++d) {
+        const uint32_t sel = 0x40u + 0x11u * d;  // byte d of both
+        const uint32_t lo = __byte_perm(__byte_perm(f[0], f[2], sel), __byte_perm(f[4], f[6], sel), 0x5410);
+        const uint32_t hi = __byte_perm(__byte_perm(f[1], f[3], sel), __byte_perm(f[5], f[7], sel), 0x5410);
+        int sum = __dp4a(static_cast<int>(lo), 0x01010101, __dp4a(static_cast<int>(hi), 0x01010101, 0));
+#pragma unroll
+        for (int o = G / 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const int col = 3 * m + d;
+        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(X.x + col * L.x_pitch + 8 * (c * 32 + lane)), "r"(lo),
+                     "r"(hi)
+                     : "memory");
+        if (lane % (G / 8) == 0)
+          sts_f1(X.off + ((c * (W4_CHUNK / G) + lane / (G / 8)) * (NT * 8) + col) * 4, -(W4_MAGIC + 8 * sum));
+        if (lane == d) sts_f1(X.fac + (c * (NT * 8) + col) * 4, __fdiv_rn(static_cast<float>(1 << (8 * d)), up));
+      }
     }
+  }
+}
+
+// N words at a shared-memory address.
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t (&w)[N], uint32_t a) {
+  if constexpr (N == 1) {
+    w[0] = lds32(a);
+  } else if constexpr (N == 2) {
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                   : "r"(a + 4 * i));
   }
 }
 
 template <int NT, int G>
 __global__ void __launch_bounds__(W4_THREADS, 1)
     linear_w4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_scales,
-                     const W4Launch L) {
+                     const __grid_constant__ W4Launch L) {
   extern __shared__ uint8_t w4_raw[];
-  __shared__ uint64_t full[W4_MAX_STAGES], empty[W4_MAX_STAGES];
-  __shared__ int abort_flag;
-  constexpr int GPC = W4_CHUNK / G;                    // groups per chunk
-  constexpr int SC_STAGE = W4_WARPS * 16 * GPC * 2;    // scale bytes per stage
+  constexpr int ROWS = w4_rows(NT), H = ROWS / 16;   // rows per warp, 16-row operands
+  constexpr int STAGE = ROWS * W4_CHUNK / 2;         // code bytes per stage
+  constexpr int RED_LD = ROWS + 4;                   // floats between columns of a warp's sums: few bank conflicts
+  __shared__ uint64_t full[W4_WARPS][W4_MAX_STAGES];
+  __shared__ int abort_flag, bad[W4_MAX_ROWS];
+  constexpr int GPC = W4_CHUNK / G;              // groups per chunk
+  constexpr int WORDS = G / 32;                  // words of a lane per row and group
+  constexpr int SC_STAGE = (ROWS * GPC * 2 + 127) / 128 * 128;  // scale bytes per stage
   const W4Params& p = L.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rw_n = L.rw, kw_n = W4_WARPS / rw_n;
+  const int rw = warp % rw_n, kw = warp / rw_n;
   const uint32_t base = (smem_u32(w4_raw) + 1023u) & ~1023u;
-  const uint32_t sc_base = base + L.stages * W4_STAGE;
-  const uint32_t red_base = sc_base + L.stages * SC_STAGE;
-  const uint32_t xs = red_base + W4_WARPS * NT * 8 * W4_RED_LD * 4;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < L.stages; ++i) {
-      mbar_init(smem_u32(&full[i]), 1);
-      mbar_init(smem_u32(&empty[i]), W4_WARPS);
-    }
-    abort_flag = 0;
+  const uint32_t codes_s = base + warp * L.stages * STAGE;
+  const uint32_t sc_s = base + W4_WARPS * L.stages * STAGE + warp * L.stages * SC_STAGE;
+  const uint32_t red_base = base + W4_WARPS * L.stages * (STAGE + SC_STAGE);
+  const int m0 = blockIdx.y * L.rows_m, rows = min(L.rows_m, p.M - m0), cols = 3 * rows;
+  W4X X;
+  X.x = red_base + W4_WARPS * NT * 8 * RED_LD * 4;
+  X.fac = X.x + 3 * L.rows_m * L.x_pitch;
+  X.off = X.fac + L.seg_chunks * NT * 32;
+  if (threadIdx.x < W4_MAX_ROWS) bad[threadIdx.x] = 0;
+  if (threadIdx.x == 0) abort_flag = 0;
+  if (lane == 0) {
+    for (int i = 0; i < L.stages; ++i) mbar_init(smem_u32(&full[warp][i]), 1);
     fence_mbar_init();
   }
-  __syncthreads();
-  const int stages_per_tile = (L.chunks + kw_n - 1) / kw_n;
 
-  if (warp == W4_WARPS) {  // producer: one thread streams the tiles' stages in order
-    if (lane != 0) return;
+  const uint32_t bar0 = smem_u32(&full[warp][0]);
+  // this warp's stages in order: tile by tile, its chunks kw, kw + KW, ...
+  int ld_tile = kw < L.chunks ? blockIdx.x : L.tiles, ld_chunk = kw, ld_st = 0;  // the next to load (lane 0)
+  auto load_next = [&] {
+    if (ld_tile >= L.tiles) return;
+    const int n0 = (ld_tile * rw_n + rw) * ROWS;
+    const uint32_t bar = bar0 + 8 * ld_st;
+    mbar_arrive_expect_tx(bar, STAGE + ROWS * GPC * 2);
+    tma_load_2d(codes_s + ld_st * STAGE, &tm_codes, bar, ld_chunk * (W4_CHUNK / 2), n0);
+    tma_load_2d(sc_s + ld_st * SC_STAGE, &tm_scales, bar, n0, ld_chunk * GPC);
+    if (++ld_st == L.stages) ld_st = 0;
+    ld_chunk += kw_n;
+    if (ld_chunk >= L.chunks) {
+      ld_chunk = kw;
+      ld_tile += gridDim.x;
+    }
+  };
+  if (lane == 0) {
     prefetch_tmap(&tm_codes);
     prefetch_tmap(&tm_scales);
-    int st = 0;
-    uint32_t ph = 0;
-    for (int tile = blockIdx.x; tile < L.tiles; tile += gridDim.x) {
-      const int n0 = tile * rw_n * 16;
-      for (int s = 0; s < stages_per_tile; ++s) {
-        if (!mbar_wait(smem_u32(&empty[st]), ph ^ 1u, p.err, &abort_flag)) {
-          const uint64_t t0 = globaltimer();  // copies in flight land before the CTA ends
-          while (globaltimer() - t0 < 200000ull) {
-          }
-          return;
-        }
-        const int nc = min(kw_n, L.chunks - s * kw_n);
-        mbar_arrive_expect_tx(smem_u32(&full[st]), nc * rw_n * 2048 + SC_STAGE);
-        for (int c = 0; c < nc; ++c)
-          tma_load_2d(base + st * W4_STAGE + c * rw_n * 2048, &tm_codes, smem_u32(&full[st]),
-                      (s * kw_n + c) * (W4_CHUNK / 2), n0);
-        tma_load_2d(sc_base + st * SC_STAGE, &tm_scales, smem_u32(&full[st]), n0, s * kw_n * GPC);
-        if (++st == L.stages) {
-          st = 0;
-          ph ^= 1u;
-        }
-      }
-    }
-    return;
+    for (int i = 0; i < L.stages; ++i) load_next();
   }
+  __syncwarp();
 
-  auto consumers_sync = [] { asm volatile("bar.sync 1, %0;" ::"r"(32 * W4_WARPS) : "memory"); };
-  const int rw = warp % rw_n, kw = warp / rw_n;
   const int g = lane >> 2, t = lane & 3;
-  const int cols = L.rows_m * L.parts;
+  // the row (of 8) that g stands for: the lanes of one bank cycle (32, 16, 8
+  // at 4, 8, 16 bytes a lane) must differ in the 16-byte piece they read
+  const int r8 = WORDS == 1 ? g : WORDS == 2 ? 2 * (g & 3) + (g >> 2) : 4 * (g & 1) + (g >> 1);
   uint32_t xcol[NT];  // this lane's column of each 8-column block; those past the last repeat it, unused
 #pragma unroll
-  for (int i = 0; i < NT; ++i) xcol[i] = xs + min(8 * i + g, cols - 1) * L.x_pitch + 16 * t;
-  const uint32_t red = red_base + warp * NT * 8 * W4_RED_LD * 4;
-  const int seg_k = L.seg_chunks * W4_CHUNK;
+  for (int i = 0; i < NT; ++i) xcol[i] = X.x + min(8 * i + g, cols - 1) * L.x_pitch + 8 * WORDS * t;
+  // this lane's bytes of group 0 in row r8 of a stage; group gi is at ^ (gi * 16 * WORDS)
+  const uint32_t mine = r8 * 128 + ((((WORDS * t) >> 2) ^ r8) << 4) + 4 * ((WORDS * t) & 3);
+  const uint32_t red = red_base + warp * NT * 8 * RED_LD * 4;
+  int4 magic;  // four registers of their own: the first sum of a group starts from them
+  asm volatile("mov.b32 %0, %4; mov.b32 %1, %4; mov.b32 %2, %4; mov.b32 %3, %4;"
+               : "=r"(magic.x), "=r"(magic.y), "=r"(magic.z), "=r"(magic.w)
+               : "n"(W4_MAGIC_BITS));
   bool ok = true;
   int st = 0;
   uint32_t ph = 0;
   if (L.segs == 1) {
-    w4_stage_x(L, xs, 0, seg_k);
-    consumers_sync();
+    __syncthreads();  // bad[] is clear
+    w4_stage_x<G, NT>(L, m0, rows, X, bad, 0, L.seg_chunks);
+    __syncthreads();  // (segs > 1: at the first part, before the first wait too)
   }
   for (int tile = blockIdx.x; tile < L.tiles; tile += gridDim.x) {
-    float acc[NT][4];
+    uint64_t acc[H][NT][2];  // pairs of columns, rows r8 and r8 + 8
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int h = 0; h < H; ++h)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
-    for (int s = 0; s < stages_per_tile; ++s) {
-      const int chunk = s * kw_n + kw;
-      if (L.segs > 1 && (s * kw_n) % L.seg_chunks == 0) {  // x no longer fits whole: its next part
-        consumers_sync();
-        w4_stage_x(L, xs, s * kw_n * W4_CHUNK, seg_k);
-        consumers_sync();
+      for (int i = 0; i < NT; ++i) acc[h][i][0] = acc[h][i][1] = 0;
+    int xc = kw;  // the chunk's place in the part of x at hand
+    for (int chunk = 0; chunk < L.chunks; chunk += kw_n, xc += kw_n) {
+      if (L.segs > 1 && chunk % L.seg_chunks == 0) {  // x does not fit whole: its next part
+        __syncthreads();
+        w4_stage_x<G, NT>(L, m0, rows, X, bad, chunk * W4_CHUNK, L.seg_chunks);
+        __syncthreads();
+        xc = kw;
       }
-      if (ok) ok = mbar_wait(smem_u32(&full[st]), ph, p.err, &abort_flag);
-      if (ok && chunk < L.chunks) {
-        const uint32_t row = base + st * W4_STAGE + kw * rw_n * 2048 + (rw * 16 + g) * 128 + 4 * t;
-        const uint32_t sc = sc_base + st * SC_STAGE + (kw * GPC * rw_n * 16 + rw * 16 + g) * 2;
-        const uint32_t xk = (chunk % L.seg_chunks) * (W4_CHUNK * 2);
+      if (chunk + kw >= L.chunks) break;  // a last step that has no chunk for this warp
+      if (ok) ok = mbar_wait(bar0 + 8 * st, ph, p.err, &abort_flag);
+      if (ok) {
+        const uint32_t row = codes_s + st * STAGE + mine;
+        const uint32_t sc = sc_s + st * SC_STAGE + 2 * r8;
+        uint32_t xk[NT];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) xk[i] = xcol[i] + xc * W4_CHUNK;
+        const uint32_t off = X.off + (xc * GPC * (NT * 8) + 2 * t) * 4;
+        uint64_t part[H][NT][2];  // the chunk's sums, before the factor of x
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+          for (int i = 0; i < NT; ++i) part[h][i][0] = part[h][i][1] = 0;
 #pragma unroll
         for (int gi = 0; gi < GPC; ++gi) {
-          float sum[NT][4];
+          int sum[H][NT][4];
+          uint32_t w[2 * H][WORDS];  // rows r8, r8 + 8, ...
+          uint32_t b[NT][2 * WORDS];
 #pragma unroll
-          for (int i = 0; i < NT; ++i)
+          for (int q = 0; q < 2 * H; ++q) lds_words<WORDS>(w[q], (row ^ (gi * 16 * WORDS)) + q * 8 * 128);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sum[i][e] = 0.f;
+          for (int i = 0; i < NT; ++i) lds_words<2 * WORDS>(b[i], xk[i] + gi * G);
 #pragma unroll
-          for (int j = 0; j < G / 32; ++j) {
-            const int c = gi * (G / 32) + j;  // 32 columns, a 16-byte piece of a row
-            const uint32_t off = static_cast<uint32_t>(c ^ g) << 4;
-            const uint32_t w0 = lds32(row + off), w1 = lds32(row + 8 * 128 + off);
-            const uint32_t a0 = w4_pair(w0), a1 = w4_pair(w1), a2 = w4_pair(w0 >> 4), a3 = w4_pair(w1 >> 4);
-            const uint32_t a4 = w4_pair(w0 >> 8), a5 = w4_pair(w1 >> 8), a6 = w4_pair(w0 >> 12),
-                           a7 = w4_pair(w1 >> 12);
+          for (int j = 0; j < WORDS; ++j)
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-              const uint4 b = lds128(xcol[i] + xk + 64 * c);
-              mma_16816(sum[i], a0, a1, a2, a3, b.x, b.y);
-              mma_16816(sum[i], a4, a5, a6, a7, b.z, b.w);
+            for (int h = 0; h < H; ++h) {
+              const uint32_t w0 = w[2 * h][j], w1 = w[2 * h + 1][j];
+              const uint32_t a0 = w0 & 0x0F0F0F0Fu, a1 = w1 & 0x0F0F0F0Fu;
+              const uint32_t a2 = (w0 >> 4) & 0x0F0F0F0Fu, a3 = (w1 >> 4) & 0x0F0F0F0Fu;
+#pragma unroll
+              for (int i = 0; i < NT; ++i) {
+                int(&d)[4] = sum[h][i];
+                if (j == 0) mma_16832(d, a0, a1, a2, a3, b[i][0], b[i][1], magic.x, magic.y, magic.z, magic.w);
+                else mma_16832(d, a0, a1, a2, a3, b[i][2 * j], b[i][2 * j + 1], d[0], d[1], d[2], d[3]);
+              }
             }
-          }
-          const float s0 = lds_bf16(sc + gi * rw_n * 32), s1 = lds_bf16(sc + gi * rw_n * 32 + 16);
+          float sc8[2 * H];  // scales of the rows
+#pragma unroll
+          for (int q = 0; q < 2 * H; ++q) sc8[q] = lds_bf16(sc + gi * (2 * ROWS) + 16 * q);
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
-            acc[i][0] += s0 * sum[i][0];
-            acc[i][1] += s0 * sum[i][1];
-            acc[i][2] += s1 * sum[i][2];
-            acc[i][3] += s1 * sum[i][3];
+            const uint64_t o = lds_u64(off + (gi * (NT * 8) + 8 * i) * 4);
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                part[h][i][e] = w4_fma2(w4_pack2(sc8[2 * h + e], sc8[2 * h + e]),
+                                        w4_add2(w4_pack2(__int_as_float(sum[h][i][2 * e]),
+                                                         __int_as_float(sum[h][i][2 * e + 1])), o),
+                                        part[h][i][e]);
+            }
           }
         }
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          const uint64_t f = lds_u64(X.fac + (xc * (NT * 8) + 8 * i + 2 * t) * 4);
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) acc[h][i][e] = w4_fma2(f, part[h][i][e], acc[h][i][e]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) load_next();  // into the stage just read
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&empty[st]));
       if (++st == L.stages) {
         st = 0;
         ph ^= 1u;
       }
     }
-    // the tile's sums: columns of 16 rows per warp, then over the KW warps and the pieces of each row of x
-    if (kw_n > 1) consumers_sync();  // the last tile's are read
+    // the tile's sums: a warp's rows by columns, then over the KW warps and the pieces of each row of x
+    if (kw_n > 1) __syncthreads();  // the last tile's are read
     else __syncwarp();
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const uint32_t a = red + ((8 * i + 2 * t) * W4_RED_LD + g) * 4;
-      asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(acc[i][0]) : "memory");
-      asm volatile("st.shared.f32 [%0], %1;" ::"r"(a + W4_RED_LD * 4), "f"(acc[i][1]) : "memory");
-      asm volatile("st.shared.f32 [%0], %1;" ::"r"(a + 32), "f"(acc[i][2]) : "memory");
-      asm volatile("st.shared.f32 [%0], %1;" ::"r"(a + W4_RED_LD * 4 + 32), "f"(acc[i][3]) : "memory");
-    }
-    if (kw_n > 1) consumers_sync();
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const uint32_t a = red + ((8 * i + 2 * t) * RED_LD + 16 * h + r8) * 4;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          sts_f1(a + 32 * e, __uint_as_float(static_cast<uint32_t>(acc[h][i][e])));
+          sts_f1(a + 32 * e + RED_LD * 4, __uint_as_float(static_cast<uint32_t>(acc[h][i][e] >> 32)));
+        }
+      }
+    if (kw_n > 1) __syncthreads();
     else __syncwarp();
-    // rows of the tile this warp finishes: all warps share a KW > 1 tile's, else each its own 16
-    const int span = kw_n > 1 ? rw_n * 16 : 16;
-    const int first = kw_n > 1 ? threadIdx.x : lane, step = kw_n > 1 ? 32 * W4_WARPS : 32;
-    for (int i = first; i < span * L.rows_m; i += step) {
-      const int m = i / span, r = i - m * span + (kw_n > 1 ? 0 : rw * 16);
-      const int n = tile * rw_n * 16 + r;
+    // all warps finish a KW > 1 tile's rows, else each its own
+    const int sh = __ffs(kw_n > 1 ? rw_n * ROWS : ROWS) - 1, span = 1 << sh;
+    const int first = kw_n > 1 ? threadIdx.x : lane, step = kw_n > 1 ? W4_THREADS : 32;
+    for (int i = first; i < span * rows; i += step) {
+      const int m = i >> sh, r = (i & (span - 1)) + (kw_n > 1 ? 0 : rw * ROWS);
+      const int n = tile * rw_n * ROWS + r;
       if (n >= p.N || !ok) continue;
       float v = 0.f;
-      for (int part = 0; part < L.parts; ++part)
-        for (int k = 0; k < kw_n; ++k)
-          v += __uint_as_float(lds32(red_base + (((k * rw_n + r / 16) * NT * 8 + m * L.parts + part) * W4_RED_LD +
-                                                 r % 16) * 4));
+      if (bad[m]) {
+        v = w4_plain_sum(p, m0 + m, n);
+      } else {
+        for (int d = 0; d < 3; ++d)
+          for (int k = 0; k < kw_n && k < L.chunks; ++k)
+            v += __uint_as_float(lds32(red_base + (((k * rw_n + r / ROWS) * NT * 8 + 3 * m + d) * RED_LD +
+                                                   r % ROWS) * 4));
+      }
       if (p.bias) v += p.bias[n];
-      w4_store(p.out, p.out_f32, static_cast<size_t>(L.m0 + m) * p.out_stride + n, v);
+      w4_store(p.out, p.out_f32, static_cast<size_t>(m0 + m) * p.out_stride + n, v);
+    }
+  }
+  if (!ok) {  // copies in flight land before the CTA ends
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < 200000ull) {
     }
   }
 }
 
 template <int NT, int G>
 static cudaError_t linear_w4_launch(const W4Launch& L, const CUtensorMap& tc, const CUtensorMap& ts, size_t smem,
-                                    int grid, cudaStream_t s) {
+                                    dim3 grid, cudaStream_t s) {
   static uint64_t done = 0;  // one bit per device: the kernel's shared-memory opt-in
   int dev = 0;
   cudaGetDevice(&dev);
   if (!((done >> dev) & 1u)) {
     const cudaError_t e =
-        cudaFuncSetAttribute(linear_w4_kernel<NT, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, W4_SMEM_MAX - 1024);
+        cudaFuncSetAttribute(linear_w4_kernel<NT, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, W4_SMEM_MAX - 2048);
     if (e != cudaSuccess) return e;
     done |= uint64_t(1) << dev;
   }
@@ -387,62 +549,61 @@ cudaError_t launch_linear_w4(const W4Params& p, cudaStream_t s) {
   W4Launch L;
   L.p = p;
   L.chunks = (row_bytes + W4_CHUNK / 2 - 1) / (W4_CHUNK / 2);
-  L.parts = p.x_f32 || p.silu ? 3 : 1;
-  const int most = W4_MAX_NT * 8 / L.parts;
-  const int passes = (p.M + most - 1) / most, per_pass = (p.M + passes - 1) / passes;
-  const int stage = W4_STAGE + W4_WARPS * 16 * (W4_CHUNK / p.group) * 2;
-  for (L.m0 = 0; L.m0 < p.M; L.m0 += per_pass) {
-    L.rows_m = p.M - L.m0 < per_pass ? p.M - L.m0 : per_pass;
-    const int cols = L.rows_m * L.parts, nt = (cols + 7) / 8;
-    const int fixed = W4_WARPS * nt * 8 * W4_RED_LD * 4 + 2048;  // sums, alignment, static barriers
-    // x lies in shared memory whole if three stages fit beside it, else in
-    // parts of `seg` chunks, a multiple of the chunks of a stage
-    const int room = (W4_SMEM_MAX - fixed - 3 * stage) / cols - 64;  // bytes per column
-    const bool whole = L.chunks * W4_CHUNK * 2 <= room;
-    // the split with the least time on the busiest SM: rounds of tiles, each a
-    // chunk time per stage, the tile's bytes and a fixed end
-    float best = 0.f;
-    L.rw = 0;
-    for (int rw = W4_WARPS; rw >= 1; rw /= 2) {
-      const int tiles = (p.N + rw * 16 - 1) / (rw * 16), kw = W4_WARPS / rw;
-      if (!whole && kw * W4_CHUNK * 2 > room) break;
-      const float cost = static_cast<float>((tiles + sms - 1) / sms) *
-                         (0.5f * ((L.chunks + kw - 1) / kw) + 0.5f * rw * L.chunks / W4_WARPS + 0.5f);
-      if (L.rw == 0 || cost < best) {
-        best = cost;
-        L.rw = rw;
-        L.tiles = tiles;
-      }
+  L.x_vec = (reinterpret_cast<uintptr_t>(p.x) & 15) == 0 && p.K % 8 == 0;
+  const int passes = (p.M + W4_MAX_ROWS - 1) / W4_MAX_ROWS;
+  L.rows_m = (p.M + passes - 1) / passes;
+  const int cols = 3 * L.rows_m, nt = (cols + 7) / 8, rows = w4_rows(nt);
+  const int stage = W4_WARPS * (rows * W4_CHUNK / 2 + (rows * (W4_CHUNK / p.group) * 2 + 127) / 128 * 128);
+  const int fixed = W4_WARPS * nt * 8 * (rows + 4) * 4 + 3072;  // sums, alignment, static barriers
+  // x lies in shared memory whole if two stages fit beside it, else in parts
+  // of `seg` chunks, a multiple of the chunks that share a row; columns are
+  // spaced so that the lanes of a bank cycle differ
+  const int pad = p.group == 32 ? 32 : p.group == 64 ? 64 : 16;
+  const int chunk_bytes = cols * W4_CHUNK + nt * 32 * (1 + W4_CHUNK / p.group);
+  const int room = (W4_SMEM_MAX - fixed - 2 * stage - cols * pad) / chunk_bytes;  // chunks
+  const bool whole = L.chunks <= room;
+  const int per = passes < sms ? sms / passes : 1;  // CTAs per part of x's rows
+  // the split with the least time on the busiest SM: rounds of tiles, each a
+  // chunk time per stage, the tile's bytes and a fixed end
+  float best = 0.f;
+  L.rw = 0;
+  for (int rw = W4_WARPS; rw >= 1; rw /= 2) {
+    const int tiles = (p.N + rw * rows - 1) / (rw * rows), kw = W4_WARPS / rw;
+    if (!whole && kw > room) break;
+    const float cost = static_cast<float>((tiles + per - 1) / per) *
+                       (0.5f * ((L.chunks + kw - 1) / kw) + 0.5f * rw * L.chunks / W4_WARPS + 0.5f);
+    if (L.rw == 0 || cost < best) {
+      best = cost;
+      L.rw = rw;
+      L.tiles = tiles;
     }
-    if (L.rw == 0) return cudaErrorInvalidValue;
-    const int kw = W4_WARPS / L.rw;
-    L.seg_chunks = whole ? L.chunks : room / (W4_CHUNK * 2) / kw * kw;
-    L.segs = (L.chunks + L.seg_chunks - 1) / L.seg_chunks;
-    L.x_pitch = L.seg_chunks * W4_CHUNK * 2 + 64;
-    const int left = W4_SMEM_MAX - fixed - cols * L.x_pitch;
-    L.stages = left / stage < W4_MAX_STAGES ? left / stage : W4_MAX_STAGES;
-    const size_t smem = fixed - 1024 + static_cast<size_t>(cols) * L.x_pitch + static_cast<size_t>(L.stages) * stage;
-    CUtensorMap tc, ts;
-    if (!encode_tmap_2d(&tc, p.codes, row_bytes, p.N, row_bytes, W4_CHUNK / 2, L.rw * 16, true) ||
-        !encode_tmap_2d(&ts, p.scales, p.N, groups, static_cast<uint64_t>(p.scale_stride) * 2, L.rw * 16,
-                        kw * (W4_CHUNK / p.group), false, 0))
-      return cudaErrorInvalidValue;
-    const int grid = L.tiles < sms ? L.tiles : sms;
-    cudaError_t e = cudaErrorInvalidValue;
-#define AF_W4_CASE(NT_)                                                                     \
-  if (nt == NT_) {                                                                          \
-    e = p.group == 32   ? linear_w4_launch<NT_, 32>(L, tc, ts, smem, grid, s)               \
-        : p.group == 64 ? linear_w4_launch<NT_, 64>(L, tc, ts, smem, grid, s)               \
-                        : linear_w4_launch<NT_, 128>(L, tc, ts, smem, grid, s);             \
   }
-    AF_W4_CASE(1)
-    AF_W4_CASE(2)
-    AF_W4_CASE(3)
-    AF_W4_CASE(4)
+  if (L.rw == 0 || passes > 65535) return cudaErrorInvalidValue;
+  const int kw = W4_WARPS / L.rw;
+  L.seg_chunks = whole ? L.chunks : room / kw * kw;
+  L.segs = (L.chunks + L.seg_chunks - 1) / L.seg_chunks;
+  L.x_pitch = L.seg_chunks * W4_CHUNK + pad;
+  const int x_bytes = cols * pad + L.seg_chunks * chunk_bytes;
+  const int left = W4_SMEM_MAX - fixed - x_bytes;
+  L.stages = left / stage < W4_MAX_STAGES ? left / stage : W4_MAX_STAGES;
+  const size_t smem = fixed - 2048 + static_cast<size_t>(x_bytes) + static_cast<size_t>(L.stages) * stage;
+  CUtensorMap tc, ts;
+  if (!encode_tmap_2d(&tc, p.codes, row_bytes, p.N, row_bytes, W4_CHUNK / 2, rows, true) ||
+      !encode_tmap_2d(&ts, p.scales, p.N, groups, static_cast<uint64_t>(p.scale_stride) * 2, rows,
+                      W4_CHUNK / p.group, false, 0))
+    return cudaErrorInvalidValue;
+  const dim3 grid(L.tiles < per ? L.tiles : per, passes);
+#define AF_W4_CASE(NT_)                                                            \
+  if (nt == NT_)                                                                   \
+    return p.group == 32   ? linear_w4_launch<NT_, 32>(L, tc, ts, smem, grid, s)   \
+           : p.group == 64 ? linear_w4_launch<NT_, 64>(L, tc, ts, smem, grid, s)   \
+                           : linear_w4_launch<NT_, 128>(L, tc, ts, smem, grid, s);
+  AF_W4_CASE(1)
+  AF_W4_CASE(2)
+  AF_W4_CASE(3)
+  AF_W4_CASE(4)
 #undef AF_W4_CASE
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace af

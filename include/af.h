@@ -410,8 +410,11 @@ af_status af_dequantize_rows_w4(const uint8_t* codes, const uint16_t* scales, in
 
 /* out[m, n] = bias[n] + sum_k f(x[m, k]) value(n, k), f = SiLU if silu != 0,
  * else the identity: the adaLN-Zero modulations W silu(temb) ([ARCH]
- * §联合注意力块) and other projections of a few rows.  x (and silu(x)) enter
- * unrounded, sums are kept in fp32.
+ * §联合注意力块) and other projections of a few rows.  f(x) enters as 24-bit
+ * fixed point with one factor per row and 256 columns: off by at most 2^-24 of
+ * the largest magnitude there (magnitudes below 2^-127 count as zero).
+ * Sums of a group are exact, everything else fp32; a row of x with an infinity or
+ * NaN is summed term by term in fp32.
  *   x: device [M, K]; out: device [M, N]; bias: device float [N] or NULL.
  * out must not overlap the inputs. */
 af_status af_linear_w4(const void* x, int x_dtype, int silu, const uint8_t* codes, const uint16_t* scales,

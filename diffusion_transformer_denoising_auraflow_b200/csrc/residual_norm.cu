@@ -115,9 +115,340 @@ __global__ void __launch_bounds__(RN_THREADS) residual_norm_row_kernel(ResidualN
   }
 }
 
+// ------------------------------------------------------------------ rows in registers
+// Widths that are multiples of 8 with 16-byte aligned tensors: TG threads per
+// row, a thread holding V vectors of eight neighbouring columns in registers
+// from the load to the stores, so HBM sees each tensor once.  A CTA stays
+// within one sample, whose factors
+//   r gate post_weight,   pre_weight (1 + scale),   shift
+// it keeps in shared memory (from the tensors each time they would take three
+// times the row's own bytes); a CTA with one round of rows reads them directly.
+// The next row's loads are issued once x' is formed, under the second norm.
+// Statistics are two-pass; sums are joined by shuffles and, for rows wider
+// than a warp, through shared memory at the row group's named barrier, two
+// buffers in turn so that one barrier per sum is enough.  Packed fp32 pairs.
+__device__ __forceinline__ uint64_t rn_pack(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 rn_unpack(uint64_t r) {
+  float2 v;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(r));
+  return v;
+}
+__device__ __forceinline__ uint64_t rn_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t rn_add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t rn_mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Eight columns as stored.
+template <typename T>
+struct RnRaw {
+  uint4 q[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ RnRaw<T> rn_load8(const void* p, size_t i) {
+  RnRaw<T> r;
+  const uint4* s = reinterpret_cast<const uint4*>(static_cast<const T*>(p) + i);
+#pragma unroll
+  for (int e = 0; e < static_cast<int>(sizeof(T) / 2); ++e) r.q[e] = s[e];
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void rn_expand(const RnRaw<T>& r, uint64_t (&v)[4]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      v[2 * e] = rn_pack(__uint_as_float(r.q[e].x), __uint_as_float(r.q[e].y));
+      v[2 * e + 1] = rn_pack(__uint_as_float(r.q[e].z), __uint_as_float(r.q[e].w));
+    }
+  } else {
+    const uint32_t w[4] = {r.q[0].x, r.q[0].y, r.q[0].z, r.q[0].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = rn_pack(bf16_lo(w[e]), bf16_hi(w[e]));
+  }
+}
+template <typename T>
+__device__ __forceinline__ void rn_store8(void* p, size_t i, const uint64_t (&v)[4]) {
+  uint4* d = reinterpret_cast<uint4*>(static_cast<T*>(p) + i);
+  float2 f[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) f[e] = rn_unpack(v[e]);
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      d[e] = make_uint4(__float_as_uint(f[2 * e].x), __float_as_uint(f[2 * e].y), __float_as_uint(f[2 * e + 1].x),
+                        __float_as_uint(f[2 * e + 1].y));
+  } else {
+    d[0] = make_uint4(pack_bf16(f[0].x, f[0].y), pack_bf16(f[1].x, f[1].y), pack_bf16(f[2].x, f[2].y),
+                      pack_bf16(f[3].x, f[3].y));
+  }
+}
+
+struct RnPlan {
+  int tg, groups;  // threads per row (a power of two below 32, or whole warps), rows of a CTA at a time
+  int per;         // CTAs per sample
+  int staged;      // factors in shared memory
+};
+
+template <typename T, bool OUT8, int V>
+__global__ void __launch_bounds__(512, V == 1 ? 2 : 1)
+    residual_norm_kernel(const __grid_constant__ ResidualNormParams p, const RnPlan plan) {
+  extern __shared__ __align__(16) float factors[];  // [3][D]
+  __shared__ float red[8][2][16];                   // [row group][buffer][warp]
+  const int tg = plan.tg, warps = tg >> 5;
+  const int grp = threadIdx.x / tg, tid = threadIdx.x - grp * tg;
+  const int lane = threadIdx.x & 31, warp = tid >> 5;
+  const int b = blockIdx.x / plan.per, cta = blockIdx.x - b * plan.per;
+  const int D = p.D;
+  const size_t sample = static_cast<size_t>(b) * p.rows_per_batch;
+  const size_t mo = static_cast<size_t>(b) * p.mod_stride;
+  auto gate_of = [&](int d) {
+    float f = p.residual_scale;
+    if (p.gate) f *= p.gate[mo + d];
+    if (p.post_weight) f *= p.post_weight[d];
+    return f;
+  };
+  auto mul_of = [&](int d) {
+    float f = 1.f;
+    if (p.scale) f += p.scale[mo + d];
+    if (p.pre_weight) f *= p.pre_weight[d];
+    return f;
+  };
+  auto add_of = [&](int d) { return p.shift ? p.shift[mo + d] : 0.f; };
+  // eight columns of the factors from column c
+  auto eight = [&](int which, int c, uint64_t (&f)[4]) {
+    if (plan.staged) {
+      const float4 lo = *reinterpret_cast<const float4*>(factors + which * D + c);
+      const float4 hi = *reinterpret_cast<const float4*>(factors + which * D + c + 4);
+      f[0] = rn_pack(lo.x, lo.y);
+      f[1] = rn_pack(lo.z, lo.w);
+      f[2] = rn_pack(hi.x, hi.y);
+      f[3] = rn_pack(hi.z, hi.w);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int d = c + 2 * e;
+        f[e] = which == 0   ? rn_pack(gate_of(d), gate_of(d + 1))
+               : which == 1 ? rn_pack(mul_of(d), mul_of(d + 1))
+                            : rn_pack(add_of(d), add_of(d + 1));
+      }
+    }
+  };
+  int buf = 0;
+  auto join = [&](float s, bool max) {
+    for (int o = warps ? 16 : tg >> 1; o > 0; o >>= 1) {
+      const float t = __shfl_xor_sync(0xffffffffu, s, o);
+      s = max ? fmaxf(s, t) : s + t;
+    }
+    if (warps <= 1) return s;
+    float* r = red[grp][buf];
+    buf ^= 1;
+    if (lane == 0) r[warp] = s;
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "r"(tg) : "memory");
+    s = r[0];
+    for (int i = 1; i < warps; ++i) s = max ? fmaxf(s, r[i]) : s + r[i];
+    return s;
+  };
+  const float inv_d = 1.0f / static_cast<float>(D);
+  // the mean to take off and the factor of a norm of the V x 8 values that get(i, v) yields
+  auto stats = [&](auto get, const bool (&on)[V], int kind, uint64_t& m2, uint64_t& r2) {
+    m2 = 0;
+    r2 = rn_pack(1.f, 1.f);
+    if (kind == NORM_NONE) return;
+    if (kind == NORM_LAYER) {
+      uint64_t s = 0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        uint64_t v[4];
+        get(i, v);  // zero behind D
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s = rn_add2(s, v[e]);
+      }
+      const float2 f = rn_unpack(s);
+      const float mean = join(f.x + f.y, false) * inv_d;
+      m2 = rn_pack(-mean, -mean);
+    }
+    uint64_t q = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      uint64_t v[4];
+      get(i, v);
+      if (on[i]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint64_t c = rn_add2(v[e], m2);
+          q = rn_fma2(c, c, q);
+        }
+      }
+    }
+    const float2 f = rn_unpack(q);
+    const float r = rsqrtf(join(f.x + f.y, false) * inv_d + p.eps);
+    r2 = rn_pack(r, r);
+  };
+
+  RnRaw<T> xq[V], bq[V];
+  auto fetch = [&](int r) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      xq[i] = RnRaw<T>{};
+      bq[i] = RnRaw<T>{};
+      const int c = 8 * (i * tg + tid);
+      if (r < p.rows_per_batch && c < D) {
+        const size_t at = (sample + r) * D + c;
+        xq[i] = rn_load8<T>(p.x, at);
+        if (p.branch) bq[i] = rn_load8<T>(p.branch, at);
+      }
+    }
+  };
+  const int step = plan.per * plan.groups;
+  int r = cta * plan.groups + grp;
+  fetch(r);
+  if (plan.staged) {
+    for (int d = threadIdx.x; d < D; d += blockDim.x) {
+      factors[d] = gate_of(d);
+      factors[D + d] = mul_of(d);
+      factors[2 * D + d] = add_of(d);
+    }
+    __syncthreads();
+  }
+  // a warp's row groups go round together: first row of the warp's
+  const int ahead = warps ? 0 : lane / tg;
+  for (; r - ahead < p.rows_per_batch; r += step) {
+    const bool live = r < p.rows_per_batch;
+    bool on[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) on[i] = live && 8 * (i * tg + tid) < D;
+    uint64_t x[V][4], m2, r2;
+    if (p.branch) {
+      stats([&](int i, uint64_t (&v)[4]) { rn_expand<T>(bq[i], v); }, on, p.post, m2, r2);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        uint64_t u[4], f[4] = {0, 0, 0, 0};
+        rn_expand<T>(xq[i], x[i]);
+        rn_expand<T>(bq[i], u);
+        if (on[i]) {
+          eight(0, 8 * (i * tg + tid), f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[i][e] = rn_fma2(f[e], rn_mul2(rn_add2(u[e], m2), r2), x[i][e]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) rn_expand<T>(xq[i], x[i]);
+    }
+    fetch(r + step);
+    const size_t base = (sample + r) * D;
+    if (p.x_out) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (on[i]) rn_store8<T>(p.x_out, base + 8 * (i * tg + tid), x[i]);
+    }
+    if (!p.y) continue;
+    stats([&](int i, uint64_t (&v)[4]) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = x[i][e];
+    }, on, p.pre, m2, r2);
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (!on[i]) continue;
+      uint64_t fa[4], fs[4];
+      eight(1, 8 * (i * tg + tid), fa);
+      eight(2, 8 * (i * tg + tid), fs);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[i][e] = rn_fma2(rn_mul2(rn_add2(x[i][e], m2), r2), fa[e], fs[e]);
+        if constexpr (OUT8) {
+          const float2 f = rn_unpack(x[i][e]);
+          amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      }
+      if constexpr (!OUT8) rn_store8<T>(p.y, base + 8 * (i * tg + tid), x[i]);
+    }
+    if constexpr (OUT8) {
+      amax = join(amax, true);
+      const float inv = amax > 0.f ? 448.0f / amax : 1.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (!on[i]) continue;
+        float2 f[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = rn_unpack(x[i][e]);
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + base + 8 * (i * tg + tid)) =
+            make_uint2(pack_e4m3x4(f[0].x * inv, f[0].y * inv, f[1].x * inv, f[1].y * inv),
+                       pack_e4m3x4(f[2].x * inv, f[2].y * inv, f[3].x * inv, f[3].y * inv));
+      }
+      if (tid == 0 && live) p.yscale[sample + r] = amax > 0.f ? amax / 448.0f : 1.0f;
+    }
+  }
+}
+
 }  // namespace
 
+template <typename T, bool OUT8>
+static cudaError_t rn_launch(const ResidualNormParams& p, cudaStream_t s) {
+  static int sms = 0;
+  if (!sms) sms = device_sm_count();
+  const int n8 = p.D / 8;
+  RnPlan plan;
+  int v;
+  if (n8 <= 32) {  // rows narrower than a warp share it
+    plan.tg = 4;
+    while (plan.tg < n8) plan.tg *= 2;
+    v = 1;
+  } else {
+    // many rows: few threads with long rows each (fewer joins, more loads in
+    // flight); fewer rows than SMs: as many threads per row as there are
+    const int cap = static_cast<int64_t>(p.B) * p.rows_per_batch <= sms ? (n8 + 511) / 512 : sizeof(T) == 4 ? 3 : 4;
+    const int w = (n8 + 32 * cap - 1) / (32 * cap);
+    plan.tg = 32 * (w < 16 ? w : 16);
+    v = (n8 + plan.tg - 1) / plan.tg;
+  }
+  const int fit = 512 / plan.tg;
+  plan.groups = plan.tg > 32 && fit > 8 ? 8 : fit;
+  if (plan.groups > p.rows_per_batch && plan.tg >= 32) plan.groups = p.rows_per_batch;
+  const int threads = plan.tg * plan.groups;
+  const int most = (p.rows_per_batch + plan.groups - 1) / plan.groups;
+  const int resident = (v == 1 ? 1024 : 512) / threads;
+  const int want = (resident * sms + p.B - 1) / p.B;
+  plan.per = most < want ? most : want;
+  plan.staged = most > plan.per;
+  const unsigned grid = static_cast<unsigned>(p.B) * plan.per;
+  const size_t smem = plan.staged ? static_cast<size_t>(p.D) * 12 : 0;
+  auto launch = [&](auto kernel) {
+    if (smem > 48 * 1024) {
+      const cudaError_t e =
+          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+      if (e != cudaSuccess) return e;
+    }
+    kernel<<<grid, threads, smem, s>>>(p, plan);
+    return cudaGetLastError();
+  };
+  if (v == 1) return launch(residual_norm_kernel<T, OUT8, 1>);
+  if (v == 2) return launch(residual_norm_kernel<T, OUT8, 2>);
+  if (v == 3) return launch(residual_norm_kernel<T, OUT8, 3>);
+  return launch(residual_norm_kernel<T, OUT8, 4>);
+}
+
 cudaError_t launch_residual_norm(const ResidualNormParams& p, bool f32, cudaStream_t s) {
+  auto al = [](const void* a) { return (reinterpret_cast<uintptr_t>(a) & 15) == 0; };
+  if (p.D % 8 == 0 && al(p.x) && al(p.branch) && al(p.x_out) && al(p.y)) {
+    if (p.yscale) return f32 ? rn_launch<float, true>(p, s) : rn_launch<uint16_t, true>(p, s);
+    return f32 ? rn_launch<float, false>(p, s) : rn_launch<uint16_t, false>(p, s);
+  }
   const size_t rows = static_cast<size_t>(p.B) * p.rows_per_batch;
   const size_t smem = static_cast<size_t>(p.D) * sizeof(float);
   auto launch = [&](auto kernel) {

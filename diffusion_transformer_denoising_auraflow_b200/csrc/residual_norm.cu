@@ -123,7 +123,11 @@ __global__ void __launch_bounds__(RN_THREADS) residual_norm_row_kernel(ResidualN
 //   r gate post_weight,   pre_weight (1 + scale),   shift
 // it keeps in shared memory (from the tensors each time they would take three
 // times the row's own bytes); a CTA with one round of rows reads them directly.
-// The next row's loads are issued once x' is formed, under the second norm.
+// RING (many rows, whole warps per row): rows stream through a ring of the row
+// group in shared memory, bulk copies issued by its first thread as soon as
+// the group has a row in registers; at 3072 columns seven groups keep two rows
+// each, 168 KB, in flight.  (Without it, loads straight to registers one
+// row ahead, two 9480 x 3072 samples with both norms take 88 us against 80.)
 // Statistics are two-pass; sums are joined by shuffles and, for rows wider
 // than a warp, through shared memory at the row group's named barrier, two
 // buffers in turn so that one barrier per sum is enough.  Packed fp32 pairs.
@@ -201,18 +205,29 @@ struct RnPlan {
   int tg, groups;  // threads per row (a power of two below 32, or whole warps), rows of a CTA at a time
   int per;         // CTAs per sample
   int staged;      // factors in shared memory
+  int stages;      // RING: rows in flight per row group
 };
+constexpr int RN_SMEM_MAX = 222 * 1024;  // beside the static barriers and sums
+constexpr int RN_RING_THREADS = 672;  // 21 warps of 80 registers
+constexpr int RN_MAX_GROUPS = 21, RN_MAX_STAGES = 8;
 
-template <typename T, bool OUT8, int V>
-__global__ void __launch_bounds__(512, V == 1 ? 2 : 1)
+// EXACT: the row is exactly TG threads of V vectors, TG whole warps.
+template <typename T, bool OUT8, int V, bool EXACT, bool RING>
+__global__ void __launch_bounds__(RING ? RN_RING_THREADS : 512, V == 1 ? 2 : 1)
     residual_norm_kernel(const __grid_constant__ ResidualNormParams p, const RnPlan plan) {
-  extern __shared__ __align__(16) float factors[];  // [3][D]
-  __shared__ float red[8][2][16];                   // [row group][buffer][warp]
+  // [3][2][D / 2]: of every eight columns the first four, then the last four, so
+  // that neighbouring lanes read neighbouring 16 bytes
+  extern __shared__ __align__(16) float factors[];
+  __shared__ float red[15][2][16];  // [row group][buffer][warp]
+  __shared__ uint64_t full[RING ? RN_MAX_GROUPS : 1][RN_MAX_STAGES];
+  __shared__ int abort_flag;
   const int tg = plan.tg, warps = tg >> 5;
   const int grp = threadIdx.x / tg, tid = threadIdx.x - grp * tg;
   const int lane = threadIdx.x & 31, warp = tid >> 5;
   const int b = blockIdx.x / plan.per, cta = blockIdx.x - b * plan.per;
   const int D = p.D;
+  // a warp's vectors are neighbours, 256 columns apart: constant offsets
+  const int c0 = EXACT || warps ? 8 * (warp * (32 * V) + lane) : 8 * tid;
   const size_t sample = static_cast<size_t>(b) * p.rows_per_batch;
   const size_t mo = static_cast<size_t>(b) * p.mod_stride;
   auto gate_of = [&](int d) {
@@ -231,8 +246,8 @@ __global__ void __launch_bounds__(512, V == 1 ? 2 : 1)
   // eight columns of the factors from column c
   auto eight = [&](int which, int c, uint64_t (&f)[4]) {
     if (plan.staged) {
-      const float4 lo = *reinterpret_cast<const float4*>(factors + which * D + c);
-      const float4 hi = *reinterpret_cast<const float4*>(factors + which * D + c + 4);
+      const float4 lo = *reinterpret_cast<const float4*>(factors + which * D + c / 2);
+      const float4 hi = *reinterpret_cast<const float4*>(factors + which * D + D / 2 + c / 2);
       f[0] = rn_pack(lo.x, lo.y);
       f[1] = rn_pack(lo.z, lo.w);
       f[2] = rn_pack(hi.x, hi.y);
@@ -249,7 +264,9 @@ __global__ void __launch_bounds__(512, V == 1 ? 2 : 1)
   };
   int buf = 0;
   auto join = [&](float s, bool max) {
-    for (int o = warps ? 16 : tg >> 1; o > 0; o >>= 1) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      if (!EXACT && warps == 0 && o >= tg) continue;
       const float t = __shfl_xor_sync(0xffffffffu, s, o);
       s = max ? fmaxf(s, t) : s + t;
     }
@@ -301,36 +318,105 @@ __global__ void __launch_bounds__(512, V == 1 ? 2 : 1)
 
   RnRaw<T> xq[V], bq[V];
   auto fetch = [&](int r) {
+    if (EXACT && r >= p.rows_per_batch) return;
+    const size_t at = (sample + r) * D + c0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      xq[i] = RnRaw<T>{};
-      bq[i] = RnRaw<T>{};
-      const int c = 8 * (i * tg + tid);
-      if (r < p.rows_per_batch && c < D) {
-        const size_t at = (sample + r) * D + c;
-        xq[i] = rn_load8<T>(p.x, at);
-        if (p.branch) bq[i] = rn_load8<T>(p.branch, at);
+      if constexpr (!EXACT) {
+        xq[i] = RnRaw<T>{};
+        bq[i] = RnRaw<T>{};
+        if (r >= p.rows_per_batch || c0 + 256 * i >= D) continue;
       }
+      xq[i] = rn_load8<T>(p.x, at + 256 * i);
+      if (p.branch) bq[i] = rn_load8<T>(p.branch, at + 256 * i);
     }
   };
   const int step = plan.per * plan.groups;
-  int r = cta * plan.groups + grp;
-  fetch(r);
-  if (plan.staged) {
-    for (int d = threadIdx.x; d < D; d += blockDim.x) {
-      factors[d] = gate_of(d);
-      factors[D + d] = mul_of(d);
-      factors[2 * D + d] = add_of(d);
+  int r = cta + plan.per * grp;  // rows dealt to the CTAs in turn: their counts differ by one at most
+  const uint32_t row_bytes = D * sizeof(T), stage_bytes = p.branch ? 2 * row_bytes : row_bytes;
+  uint32_t ring = 0;  // this group's stages, behind the factors
+  auto copy_row = [&](int r, int st) {
+    const uint32_t bar = smem_u32(&full[grp][st]), dst = ring + st * stage_bytes;
+    const size_t at = (sample + r) * D;
+    mbar_arrive_expect_tx(bar, stage_bytes);
+    bulk_load(dst, static_cast<const T*>(p.x) + at, row_bytes, bar);
+    if (p.branch) bulk_load(dst + row_bytes, static_cast<const T*>(p.branch) + at, row_bytes, bar);
+  };
+  if constexpr (RING) {
+    ring = smem_u32(factors) + (plan.staged ? D * 12 : 0) + grp * plan.stages * stage_bytes;
+    if (threadIdx.x == 0) abort_flag = 0;
+    if (tid == 0) {
+      for (int i = 0; i < plan.stages; ++i) mbar_init(smem_u32(&full[grp][i]), 1);
+      fence_mbar_init();
+      for (int i = 0; i < plan.stages && r + i * step < p.rows_per_batch; ++i) copy_row(r + i * step, i);
     }
-    __syncthreads();
+  } else {
+    fetch(r);
   }
+  if (plan.staged) {
+    for (int d = 4 * threadIdx.x; d < D; d += 4 * blockDim.x) {  // four columns: their loads overlap
+      const int at = (d & 4 ? D / 2 : 0) + (d >> 3) * 4;
+      float f[3][4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        f[0][e] = gate_of(d + e);
+        f[1][e] = mul_of(d + e);
+        f[2][e] = add_of(d + e);
+      }
+#pragma unroll
+      for (int w = 0; w < 3; ++w)
+        *reinterpret_cast<float4*>(factors + w * D + at) = make_float4(f[w][0], f[w][1], f[w][2], f[w][3]);
+    }
+  }
+  if (RING || plan.staged) __syncthreads();
   // a warp's row groups go round together: first row of the warp's
-  const int ahead = warps ? 0 : lane / tg;
+  const int ahead = warps ? 0 : lane / tg * plan.per;
+  int st = 0;
+  uint32_t ph = 0;
   for (; r - ahead < p.rows_per_batch; r += step) {
+    if constexpr (RING) {
+      const bool got = mbar_wait(smem_u32(&full[grp][st]), ph, nullptr, &abort_flag);
+      const uint32_t src = ring + st * stage_bytes + c0 * sizeof(T);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const bool in = EXACT || c0 + 256 * i < D;
+#pragma unroll
+        for (int e = 0; e < static_cast<int>(sizeof(T) / 2); ++e) {
+          const uint32_t o = 256 * i * sizeof(T) + 16 * e;
+          xq[i].q[e] = in ? lds128(src + o) : make_uint4(0, 0, 0, 0);
+          bq[i].q[e] = in && p.branch ? lds128(src + row_bytes + o) : make_uint4(0, 0, 0, 0);
+        }
+      }
+      // the whole group has the row (or has given up): the stage is free
+      uint32_t failed;
+      if (warps == 1) {
+        failed = __any_sync(0xffffffffu, !got);
+      } else {
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t"
+            "setp.ne.u32 p, %1, 0;\n\t"
+            "bar.red.or.pred q, %2, %3, p;\n\t"
+            "selp.u32 %0, 1, 0, q;\n\t}"
+            : "=r"(failed)
+            : "r"(static_cast<uint32_t>(!got)), "r"(1 + grp), "r"(tg)
+            : "memory");
+      }
+      if (failed) {  // copies in flight land before the CTA ends
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 200000ull) {
+        }
+        return;
+      }
+      if (tid == 0 && r + plan.stages * step < p.rows_per_batch) copy_row(r + plan.stages * step, st);
+      if (++st == plan.stages) {
+        st = 0;
+        ph ^= 1u;
+      }
+    }
     const bool live = r < p.rows_per_batch;
     bool on[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) on[i] = live && 8 * (i * tg + tid) < D;
+    for (int i = 0; i < V; ++i) on[i] = EXACT || (live && c0 + 256 * i < D);
     uint64_t x[V][4], m2, r2;
     if (p.branch) {
       stats([&](int i, uint64_t (&v)[4]) { rn_expand<T>(bq[i], v); }, on, p.post, m2, r2);
@@ -340,21 +426,24 @@ __global__ void __launch_bounds__(512, V == 1 ? 2 : 1)
         rn_expand<T>(xq[i], x[i]);
         rn_expand<T>(bq[i], u);
         if (on[i]) {
-          eight(0, 8 * (i * tg + tid), f);
+          eight(0, c0 + 256 * i, f);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[i][e] = rn_fma2(f[e], rn_mul2(rn_add2(u[e], m2), r2), x[i][e]);
+          for (int e = 0; e < 4; ++e) {
+            if (p.post != NORM_NONE) u[e] = rn_mul2(rn_add2(u[e], m2), r2);
+            x[i][e] = rn_fma2(f[e], u[e], x[i][e]);
+          }
         }
       }
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i) rn_expand<T>(xq[i], x[i]);
     }
-    fetch(r + step);
-    const size_t base = (sample + r) * D;
+    if constexpr (!RING) fetch(r + step);
+    const size_t base = (sample + r) * D + c0;
     if (p.x_out) {
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (on[i]) rn_store8<T>(p.x_out, base + 8 * (i * tg + tid), x[i]);
+        if (on[i]) rn_store8<T>(p.x_out, base + 256 * i, x[i]);
     }
     if (!p.y) continue;
     stats([&](int i, uint64_t (&v)[4]) {
@@ -366,8 +455,8 @@ __global__ void __launch_bounds__(512, V == 1 ? 2 : 1)
     for (int i = 0; i < V; ++i) {
       if (!on[i]) continue;
       uint64_t fa[4], fs[4];
-      eight(1, 8 * (i * tg + tid), fa);
-      eight(2, 8 * (i * tg + tid), fs);
+      eight(1, c0 + 256 * i, fa);
+      eight(2, c0 + 256 * i, fs);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         x[i][e] = rn_fma2(rn_mul2(rn_add2(x[i][e], m2), r2), fa[e], fs[e]);
@@ -376,7 +465,7 @@ __global__ void __launch_bounds__(512, V == 1 ? 2 : 1)
           amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
         }
       }
-      if constexpr (!OUT8) rn_store8<T>(p.y, base + 8 * (i * tg + tid), x[i]);
+      if constexpr (!OUT8) rn_store8<T>(p.y, base + 256 * i, x[i]);
     }
     if constexpr (OUT8) {
       amax = join(amax, true);
@@ -387,7 +476,7 @@ __global__ void __launch_bounds__(512, V == 1 ? 2 : 1)
         float2 f[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) f[e] = rn_unpack(x[i][e]);
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + base + 8 * (i * tg + tid)) =
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + base + 256 * i) =
             make_uint2(pack_e4m3x4(f[0].x * inv, f[0].y * inv, f[1].x * inv, f[1].y * inv),
                        pack_e4m3x4(f[2].x * inv, f[2].y * inv, f[3].x * inv, f[3].y * inv));
       }
@@ -397,6 +486,24 @@ __global__ void __launch_bounds__(512, V == 1 ? 2 : 1)
 }
 
 }  // namespace
+
+template <typename T, bool OUT8, int V, bool EXACT, bool RING>
+static cudaError_t rn_go(const ResidualNormParams& p, const RnPlan& plan, unsigned grid, int threads, size_t smem,
+                         cudaStream_t s) {
+  static uint64_t done = 0;  // one bit per device: the kernel's shared-memory opt-in
+  if (smem > 48 * 1024) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (!((done >> dev) & 1u)) {
+      const cudaError_t e = cudaFuncSetAttribute(residual_norm_kernel<T, OUT8, V, EXACT, RING>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, RN_SMEM_MAX);
+      if (e != cudaSuccess) return e;
+      done |= uint64_t(1) << dev;
+    }
+  }
+  residual_norm_kernel<T, OUT8, V, EXACT, RING><<<grid, threads, smem, s>>>(p, plan);
+  return cudaGetLastError();
+}
 
 template <typename T, bool OUT8>
 static cudaError_t rn_launch(const ResidualNormParams& p, cudaStream_t s) {
@@ -412,35 +519,49 @@ static cudaError_t rn_launch(const ResidualNormParams& p, cudaStream_t s) {
   } else {
     // many rows: few threads with long rows each (fewer joins, more loads in
     // flight); fewer rows than SMs: as many threads per row as there are
-    const int cap = static_cast<int64_t>(p.B) * p.rows_per_batch <= sms ? (n8 + 511) / 512 : sizeof(T) == 4 ? 3 : 4;
+    const int cap = static_cast<int64_t>(p.B) * p.rows_per_batch <= sms ? (n8 + 511) / 512 : sizeof(T) == 4 ? 2 : 4;
     const int w = (n8 + 32 * cap - 1) / (32 * cap);
     plan.tg = 32 * (w < 16 ? w : 16);
     v = (n8 + plan.tg - 1) / plan.tg;
   }
-  const int fit = 512 / plan.tg;
-  plan.groups = plan.tg > 32 && fit > 8 ? 8 : fit;
-  if (plan.groups > p.rows_per_batch && plan.tg >= 32) plan.groups = p.rows_per_batch;
-  const int threads = plan.tg * plan.groups;
-  const int most = (p.rows_per_batch + plan.groups - 1) / plan.groups;
-  const int resident = (v == 1 ? 1024 : 512) / threads;
-  const int want = (resident * sms + p.B - 1) / p.B;
-  plan.per = most < want ? most : want;
-  plan.staged = most > plan.per;
-  const unsigned grid = static_cast<unsigned>(p.B) * plan.per;
-  const size_t smem = plan.staged ? static_cast<size_t>(p.D) * 12 : 0;
-  auto launch = [&](auto kernel) {
-    if (smem > 48 * 1024) {
-      const cudaError_t e =
-          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-      if (e != cudaSuccess) return e;
-    }
-    kernel<<<grid, threads, smem, s>>>(p, plan);
-    return cudaGetLastError();
+  const int factor_bytes = p.D * 12, row_bytes = p.D * static_cast<int>(sizeof(T)) * (p.branch ? 2 : 1);
+  // rows at a time: as many as the threads give, 15 where they need a barrier
+  auto split = [&](int threads) {
+    const int fit = threads / plan.tg;
+    plan.groups = plan.tg > 32 && fit > 15 ? 15 : fit;
+    if (plan.groups > p.rows_per_batch && plan.tg >= 32) plan.groups = p.rows_per_batch;
+    return (p.rows_per_batch + plan.groups - 1) / plan.groups;  // rounds of a sample's rows
   };
-  if (v == 1) return launch(residual_norm_kernel<T, OUT8, 1>);
-  if (v == 2) return launch(residual_norm_kernel<T, OUT8, 2>);
-  if (v == 3) return launch(residual_norm_kernel<T, OUT8, 3>);
-  return launch(residual_norm_kernel<T, OUT8, 4>);
+  const int one = (sms + p.B - 1) / p.B;  // CTAs per sample at one per SM
+  plan.stages = 0;
+  int rounds = split(RN_RING_THREADS);
+  if (v > 1 && rounds > 2 * one) {
+    const int fit = (RN_SMEM_MAX - factor_bytes) / (row_bytes * plan.groups);
+    if (fit >= 2) plan.stages = fit < RN_MAX_STAGES ? fit : RN_MAX_STAGES;
+  }
+  const bool ring = plan.stages > 0;
+  if (!ring) rounds = split(512);
+  const int threads = plan.tg * plan.groups;
+  const int want = ring ? one : ((v == 1 ? 1024 : 512) / threads * sms + p.B - 1) / p.B;
+  plan.per = rounds < want ? rounds : want;
+  plan.staged = rounds > plan.per;
+  const unsigned grid = static_cast<unsigned>(p.B) * plan.per;
+  const size_t smem =
+      (plan.staged ? factor_bytes : 0) + static_cast<size_t>(plan.stages) * plan.groups * row_bytes;
+  const bool exact = plan.tg >= 32 && plan.tg * v == n8;
+#define AF_RN_CASE(V_)                                                                                         \
+  if (v == V_) {                                                                                               \
+    if (ring)                                                                                                  \
+      return exact ? rn_go<T, OUT8, V_, true, true>(p, plan, grid, threads, smem, s)                            \
+                   : rn_go<T, OUT8, V_, false, true>(p, plan, grid, threads, smem, s);                          \
+    return rn_go<T, OUT8, V_, false, false>(p, plan, grid, threads, smem, s);                                  \
+  }
+  AF_RN_CASE(1)
+  AF_RN_CASE(2)
+  AF_RN_CASE(3)
+  AF_RN_CASE(4)
+#undef AF_RN_CASE
+  return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_residual_norm(const ResidualNormParams& p, bool f32, cudaStream_t s) {

@@ -117,6 +117,54 @@ def test_matches_oracle(af, B, N, D, dtype, post, pre, gate, mod, pw, qw, r):
     assert np.all(np.abs(v - ry) <= ey + (np.abs(ry) + ey) * 2.0 ** -4 * (1 + 1e-5) + s * 2.0 ** -10)
 
 
+@pytest.mark.parametrize("dtype,y8", [(BF, False), (BF, True), (F32, False)])
+@pytest.mark.parametrize("B,N,D", [(2, 4360, 3072), (1, 3001, 1024), (3, 1100, 2048), (1, 2500, 4104), (1, 2100, 8192),
+                                   (1, 20001, 256), (1, 60007, 32), (5, 1000, 520), (1, 1300, 16384), (1, 9001, 40)])
+@pytest.mark.parametrize("post,pre,branch", [("none", "layer", True), ("layer", "rms", True), ("none", "rms", False)])
+def test_many_rows(af, B, N, D, dtype, y8, post, pre, branch):
+    """Row counts at which a CTA takes several rounds of rows (more than twice
+    what 148 SMs hold at once), against the formula in fp64 on the device."""
+    g = torch.Generator(device="cuda").manual_seed(981)
+    x = (torch.randn(B, N, D, device="cuda", generator=g) * 2 + 0.5).to(dtype)
+    b = torch.randn(B, N, D, device="cuda", generator=g).to(dtype) if branch else None
+    t = torch.randn(B, 3 * D, device="cuda", generator=g) * 0.5
+    pw = torch.randn(D, device="cuda", generator=g) * 0.2 + 1
+    full = torch.full((B * N + 1, D), 3.0, dtype=torch.uint8 if y8 else dtype, device="cuda")
+    y, xo = full[:-1].view(B, N, D), torch.empty_like(x)
+    kw = dict(shift=t[:, D:], scale=t[:, 2 * D:], mod_stride=3 * D, pre=pre, residual_scale=0.7)
+    if branch:
+        kw.update(gate=t, post=post, post_weight=pw)
+    ys = torch.empty(B * N, device="cuda")
+    if y8:
+        af.residual_norm_e4m3(x, b, xo, y, ys, EPS, **kw)
+    else:
+        af.residual_norm(x, b, xo, y, EPS, **kw)
+
+    def norm(v, kind):
+        if kind == "layer":
+            v = v - v.mean(-1, keepdim=True)
+        return v if kind == "none" else v / torch.sqrt((v * v).mean(-1, keepdim=True) + EPS)
+
+    rx = x.double()
+    if branch:
+        rx = rx + float(np.float32(0.7)) * t[:, None, :D].double() * norm(b.double(), post) * pw.double()
+    n = norm(rx, pre)
+    f = 1 + t[:, None, 2 * D:].double()
+    ry = n * f + t[:, None, D:2 * D].double()
+    # the bounds of _norm_err with the row's largest values in the place of each value's own
+    big = rx.abs().amax(-1, keepdim=True)
+    nb = n.abs().amax(-1, keepdim=True)
+    ex = (3 * C if branch else 0.0) * (big + 1)
+    ey = f.abs() * (2 * C * (nb + 1) + 3 * ex * nb) + 4 * U * ry.abs()
+    assert torch.all((xo.double() - rx).abs() <= ex + (rx.abs() + ex) * STEP[dtype])
+    if y8:
+        v = y.view(torch.float8_e4m3fn).double() * ys.double().view(B, N, 1)
+        assert torch.all((v - ry).abs() <= ey + (ry.abs() + ey) * 2.0 ** -4 * (1 + 1e-5) + ys.view(B, N, 1) * 2.0 ** -10)
+    else:
+        assert torch.all((y.double() - ry).abs() <= ey + (ry.abs() + ey) * STEP[dtype])
+    assert torch.all(full[-1].float() == 3.0)
+
+
 @pytest.mark.parametrize("D", [3072, 77, 2048])
 def test_without_branch_or_outputs(af, D):
     x, b, table, pw, qw = _inputs(2, 6, D, BF, 911)

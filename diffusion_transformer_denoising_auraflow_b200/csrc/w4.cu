@@ -26,81 +26,220 @@ __device__ __forceinline__ void w4_store(void* p, int f32, size_t i, float v) {
 __device__ __forceinline__ float w4_bf16(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
 __device__ __forceinline__ float w4_silu(float a) { return a / (1.0f + expf(-a)); }
 
+// packed fp32 pairs
+__device__ __forceinline__ uint64_t w4_pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t w4_add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t w4_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+constexpr float W4_MAGIC = 12582912.0f;    // 1.5 * 2^23: the bits of W4_MAGIC + i are its bits + i for |i| < 2^22
+
+// Eight columns of a row from column k as stored (bf16 in the first vector,
+// fp32 in both), zero behind column K, and their values.  vec: rows are whole
+// 16-byte vectors.
+struct W4Raw {
+  uint4 a, b;
+};
+__device__ __forceinline__ W4Raw w4_load8(const void* p, int f32, int vec, size_t row, int k, int K) {
+  W4Raw r{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+  if (vec) {
+    if (k < K) {
+      const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + (row + k) * (f32 ? 4 : 2));
+      r.a = s[0];
+      if (f32) r.b = s[1];
+    }
+    return r;
+  }
+  uint32_t w[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    w[e] = k + e < K ? (f32 ? static_cast<const uint32_t*>(p)[row + k + e] : static_cast<const uint16_t*>(p)[row + k + e])
+                     : 0u;
+  if (f32) {
+    r.a = make_uint4(w[0], w[1], w[2], w[3]);
+    r.b = make_uint4(w[4], w[5], w[6], w[7]);
+  } else {
+    r.a = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+  }
+  return r;
+}
+__device__ __forceinline__ void w4_values(const W4Raw& r, int f32, float (&v)[8]) {
+  const uint32_t q[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    v[e] = f32 ? __uint_as_float(q[e]) : (e & 1) ? bf16_hi(q[e / 2]) : bf16_lo(q[e / 2]);
+}
+
 // ------------------------------------------------------------------ quantiser
 // Per row and group: a = max |w|, s = bf16(a / 7) to nearest even, c = 8 +
-// the whole number nearest to w / s (ties to even), 8 where s is zero.  Both
-// divisions are IEEE fp32 ones.  They decide as real numbers would: a border
-// between two codes, (j + 1/2) s, and one between two scales, times 7, are
-// fp32 numbers (4 x 8 and 9 x 3 bits), and a w or a next to one is off it by
-// at least 2^-24 relative, which the rounded quotient still shows.
-// One warp per row; a lane takes two neighbouring columns, so a group is
-// G / 2 lanes' work: 16, 32, or 32 lanes twice.
-template <int G>
-__global__ void __launch_bounds__(256) quantize_rows_w4_kernel(const void* __restrict__ w, int f32, int N, int K,
+// the whole number nearest to w / s (ties to even), 8 where s is zero.  The
+// division by 7 is an IEEE fp32 one, and so is w / s for fp32 weights: they
+// decide as real numbers would.  A border between two codes, (j + 1/2) s, and
+// one between two scales, times 7, are fp32 numbers (4 x 8 and 9 x 3 bits),
+// and a w or a next to one is off it by at least 2^-24 relative, which the
+// rounded quotient still shows.  bf16 weights are eight bits over eight bits:
+// off a border (j + 1/2) by at least 2^-13, or on it, so w (1 / s) rounded to
+// a multiple of 2^-14 decides the same for a third of the instructions; and a
+// is never 7 times a border of s (an odd number of nine bits), so a (1 / 7) does.
+// Bound: HBM (2.5 or 4.5 bytes a weight).  A CTA takes 32 rows by 256 columns:
+// a warp reads four rows, 512 bytes of each in one load per lane, all four in
+// flight; a group is G / 8 lanes; the scales of 32 rows go out together.
+constexpr int W4Q_ROWS = 4;  // rows per warp
+
+template <int G, bool F32>
+__global__ void __launch_bounds__(256, F32 ? 4 : 6) quantize_rows_w4_kernel(const void* __restrict__ w, int vec, int N, int K,
                                                                int groups, uint8_t* __restrict__ codes,
                                                                uint16_t* __restrict__ scales, int scale_stride) {
-  const int n = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (n >= N) return;
-  uint8_t* cr = codes + static_cast<size_t>(n) * groups * (G / 2);
-  const size_t row = static_cast<size_t>(n) * K;
-  constexpr int BPL = G == 128 ? 2 : 1;      // bytes (pairs of columns) per lane and step
-  constexpr int LPG = G / 2 / BPL;           // lanes that share a group
-  for (int j = lane * BPL; j < (groups * (G / 2) + 32 * BPL - 1) / (32 * BPL) * (32 * BPL); j += 32 * BPL) {
-    float v[2 * BPL], a = 0.f;
+  __shared__ uint16_t sc[256 / G][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int chunks = (groups * G + 255) / 256, tile = blockIdx.x / chunks, chunk = blockIdx.x - tile * chunks;
+  const int n0 = tile * 32, r0 = n0 + warp * W4Q_ROWS;
+  const int k = chunk * 256 + lane * 8, g = lane / (G / 8);
+  const bool in = k < groups * G;
+  W4Raw raw[W4Q_ROWS];
 #pragma unroll
-    for (int e = 0; e < 2 * BPL; ++e) {
-      const int k = 2 * j + e;
-      v[e] = k < K ? w4_load(w, f32, row + k) : 0.f;
-      a = fmaxf(a, fabsf(v[e]));
-    }
+  for (int i = 0; i < W4Q_ROWS; ++i)  // rows behind the last repeat it, and are not written
+    raw[i] = w4_load8(w, F32, vec, static_cast<size_t>(min(r0 + i, N - 1)) * K, k, K);
 #pragma unroll
-    for (int o = LPG / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-    const uint16_t sb = static_cast<uint16_t>(pack_bf16(__fdiv_rn(a, 7.0f), 0.f));
+  for (int i = 0; i < W4Q_ROWS; ++i) {
+    float v[8];
+    w4_values(raw[i], F32, v);
+    float a = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(v[e]));
+#pragma unroll
+    for (int o = G / 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    const uint16_t sb = static_cast<uint16_t>(pack_bf16(F32 ? __fdiv_rn(a, 7.0f) : a * (1.0f / 7.0f), 0.f));
     const float s = w4_bf16(sb);
-    const int g = 2 * j / G;
-    if (g >= groups) continue;
-    if ((lane & (LPG - 1)) == 0) scales[static_cast<size_t>(g) * scale_stride + n] = sb;
+    // w / s rounded to a whole number, as a float; small scales (1 / s may
+    // overflow, few bits left) take the division
+    uint64_t c[4];  // columns 2 e and 2 e + 1
+    if (F32 || s < 0x1p-100f) {
 #pragma unroll
-    for (int b = 0; b < BPL; ++b) {
-      int c[2];
+      for (int e = 0; e < 4; ++e) {
+        float d[2];
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        c[e] = s > 0.f ? min(15, max(0, 8 + __float2int_rn(__fdiv_rn(v[2 * b + e], s)))) : 8;
-      cr[j + b] = static_cast<uint8_t>(c[0] | c[1] << 4);
+        for (int o = 0; o < 2; ++o)
+          d[o] = s > 0.f ? fminf(7.f, fmaxf(-8.f, rintf(__fdiv_rn(v[2 * e + o], s)))) : 0.f;
+        c[e] = w4_pack2(d[0], d[1]);
+      }
+    } else {
+      float inv;
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+      const uint64_t inv2 = w4_pack2(inv, inv);
+      const uint64_t snap = w4_pack2(768.0f, 768.0f), unsnap = w4_pack2(-768.0f, -768.0f);  // 768: steps of 2^-14
+      const uint64_t whole = w4_pack2(W4_MAGIC, W4_MAGIC), unwhole = w4_pack2(-W4_MAGIC, -W4_MAGIC);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        c[e] = w4_add2(w4_add2(w4_add2(w4_fma2(w4_pack2(v[2 * e], v[2 * e + 1]), inv2, snap), unsnap), whole),
+                       unwhole);
     }
+    // nibbles: columns e and e + 2 are 8 bits apart in a half word, the low 16 bits of 2^23 + their whole part;
+    // + 8 for every nibble
+    uint32_t h[4];
+    const uint64_t up = w4_pack2(256.0f, 256.0f), eights = w4_pack2(8388608.0f + 2056.0f, 8388608.0f + 2056.0f);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint64_t t = w4_add2(w4_fma2(c[2 * e + 1], up, c[2 * e]), eights);
+      h[2 * e] = static_cast<uint32_t>(t);
+      h[2 * e + 1] = static_cast<uint32_t>(t >> 32);
+    }
+    const uint32_t lo = __byte_perm(h[0], h[2], 0x5410), hi = __byte_perm(h[1], h[3], 0x5410);
+    const int n = r0 + i;
+    if (n < N && in)
+      reinterpret_cast<uint32_t*>(codes + static_cast<size_t>(n) * groups * (G / 2))[k >> 3] = lo | hi << 4;
+    if (lane % (G / 8) == 0) sc[g][warp * W4Q_ROWS + i] = sb;
   }
+  __syncthreads();
+  for (int i = threadIdx.x; i < (256 / G) * 32; i += 256) {
+    const int gi = i >> 5, n = n0 + (i & 31), at = chunk * (256 / G) + gi;
+    if (n < N && at < groups) scales[static_cast<size_t>(at) * scale_stride + n] = sc[gi][i & 31];
+  }
+}
+
+static bool w4_vec(const void* p, int K) {
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && K % 8 == 0;
 }
 
 cudaError_t launch_quantize_rows_w4(const void* w, bool f32, int N, int K, int group, uint8_t* codes,
                                     uint16_t* scales, int scale_stride, cudaStream_t s) {
-  const int groups = (K + group - 1) / group, blocks = (N + 7) / 8;
-  switch (group) {
-    case 32: quantize_rows_w4_kernel<32><<<blocks, 256, 0, s>>>(w, f32, N, K, groups, codes, scales, scale_stride); break;
-    case 64: quantize_rows_w4_kernel<64><<<blocks, 256, 0, s>>>(w, f32, N, K, groups, codes, scales, scale_stride); break;
-    case 128: quantize_rows_w4_kernel<128><<<blocks, 256, 0, s>>>(w, f32, N, K, groups, codes, scales, scale_stride); break;
-    default: return cudaErrorInvalidValue;
+  const int groups = (K + group - 1) / group;
+  const int64_t grid = static_cast<int64_t>((groups * group + 255) / 256) * ((N + 31) / 32);
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  const int vec = w4_vec(w, K);
+#define AF_Q4_CASE(G_)                                                                                              \
+  if (group == G_) {                                                                                                \
+    auto kernel = f32 ? quantize_rows_w4_kernel<G_, true> : quantize_rows_w4_kernel<G_, false>;                     \
+    kernel<<<static_cast<unsigned>(grid), 256, 0, s>>>(w, vec, N, K, groups, codes, scales, scale_stride);          \
+    return cudaGetLastError();                                                                                      \
   }
-  return cudaGetLastError();
+  AF_Q4_CASE(32)
+  AF_Q4_CASE(64)
+  AF_Q4_CASE(128)
+#undef AF_Q4_CASE
+  return cudaErrorInvalidValue;
 }
 
 // ------------------------------------------------------------------ values
+// The quantiser's tiles the other way round, bound by HBM too: a lane turns 4
+// bytes of codes into eight values.  8388608 + c is the pattern 0x4B000000 | c.
 __global__ void __launch_bounds__(256) dequantize_rows_w4_kernel(const uint8_t* __restrict__ codes,
                                                                  const uint16_t* __restrict__ scales,
                                                                  int scale_stride, int N, int K, int group,
-                                                                 void* __restrict__ out, int f32) {
-  const int n = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (n >= N) return;
-  const uint8_t* cr = codes + static_cast<size_t>(n) * ((K + group - 1) / group) * (group / 2);
-  const size_t row = static_cast<size_t>(n) * K;
-  for (int k = lane; k < K; k += 32) {
-    const int c = (cr[k >> 1] >> (4 * (k & 1))) & 15;
-    w4_store(out, f32, row + k, w4_bf16(scales[static_cast<size_t>(k / group) * scale_stride + n]) * (c - 8));
+                                                                 void* __restrict__ out, int f32, int vec) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int chunks = (K + 255) / 256, tile = blockIdx.x / chunks;
+  const int r0 = tile * 32 + warp * W4Q_ROWS, k = (blockIdx.x - tile * chunks) * 256 + lane * 8;
+  const int groups = (K + group - 1) / group;
+  if (k >= K) return;
+  uint32_t w[W4Q_ROWS];
+  float s[W4Q_ROWS];
+#pragma unroll
+  for (int i = 0; i < W4Q_ROWS; ++i) {
+    if (r0 + i >= N) break;
+    w[i] = reinterpret_cast<const uint32_t*>(codes + static_cast<size_t>(r0 + i) * groups * (group / 2))[k >> 3];
+    s[i] = w4_bf16(scales[static_cast<size_t>(k / group) * scale_stride + r0 + i]);
+  }
+#pragma unroll
+  for (int i = 0; i < W4Q_ROWS; ++i) {
+    if (r0 + i >= N) break;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      v[e] = s[i] * (__uint_as_float(((w[i] >> (4 * e)) & 15u) | 0x4B000000u) - 8388616.0f);
+    const size_t at = static_cast<size_t>(r0 + i) * K + k;
+    if (vec) {
+      uint4* d = reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) + at * (f32 ? 4 : 2));
+      if (f32) {
+        d[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+        d[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+      } else {
+        d[0] = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (k + e < K) w4_store(out, f32, at + e, v[e]);
+    }
   }
 }
 
 cudaError_t launch_dequantize_rows_w4(const uint8_t* codes, const uint16_t* scales, int scale_stride, int N, int K,
                                       int group, void* out, bool f32, cudaStream_t s) {
-  dequantize_rows_w4_kernel<<<(N + 7) / 8, 256, 0, s>>>(codes, scales, scale_stride, N, K, group, out, f32);
+  const int64_t grid = static_cast<int64_t>((K + 255) / 256) * ((N + 31) / 32);
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  dequantize_rows_w4_kernel<<<static_cast<unsigned>(grid), 256, 0, s>>>(codes, scales, scale_stride, N, K, group, out,
+                                                                       f32, w4_vec(out, K));
   return cudaGetLastError();
 }
 
@@ -155,7 +294,6 @@ struct W4Launch {
 
 constexpr float W4_FIX = 8355000.0f;       // largest fixed-point value; three signed bytes reach 8355711
 constexpr float W4_TINY = 0x1p-104f;       // a row's chunk below this counts in steps of W4_TINY / W4_FIX
-constexpr float W4_MAGIC = 12582912.0f;    // 1.5 * 2^23: the bits of W4_MAGIC + i are its bits + i for |i| < 2^22
 constexpr int W4_MAGIC_BITS = 0x4B400000;
 
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
@@ -167,22 +305,6 @@ __device__ __forceinline__ uint64_t lds_u64(uint32_t a) {
   uint64_t v;
   asm volatile("ld.shared.u64 %0, [%1];" : "=l"(v) : "r"(a));
   return v;
-}
-// packed fp32 pairs
-__device__ __forceinline__ uint64_t w4_pack2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t w4_add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t w4_fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
 }
 __device__ __forceinline__ void sts_f1(uint32_t a, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
@@ -232,45 +354,23 @@ __device__ __forceinline__ void w4_stage_x(const W4Launch& L, int m0, int rows, 
   constexpr int U = 2;  // chunks per warp whose loads are in flight together
   const int items = rows * chunks;
   for (int i0 = warp; i0 < items; i0 += U * W4_WARPS) {
-    uint4 raw[U][2];
+    W4Raw raw[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * W4_WARPS;
-      raw[u][0] = raw[u][1] = make_uint4(0, 0, 0, 0);
-      if (i >= items) continue;
-      const int m = i / chunks, k = k0 + 8 * ((i - m * chunks) * 32 + lane);
-      const size_t at = static_cast<size_t>(m0 + m) * p.K + k;
-      if (L.x_vec && k + 8 <= p.K) {
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.x) + at * (p.x_f32 ? 4 : 2));
-        raw[u][0] = src[0];
-        if (p.x_f32) raw[u][1] = src[1];
-      } else if (p.x_f32) {
-        const uint32_t* src = static_cast<const uint32_t*>(p.x) + at;
-        uint32_t w[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = k + e < p.K ? src[e] : 0u;
-        raw[u][0] = make_uint4(w[0], w[1], w[2], w[3]);
-        raw[u][1] = make_uint4(w[4], w[5], w[6], w[7]);
-      } else {
-        const uint16_t* src = static_cast<const uint16_t*>(p.x) + at;
-        uint32_t w[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = k + e < p.K ? src[e] : 0u;
-        raw[u][0] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
-      }
+      const int i = min(i0 + u * W4_WARPS, items - 1), m = i / chunks;
+      raw[u] = w4_load8(p.x, p.x_f32, L.x_vec, static_cast<size_t>(m0 + m) * p.K,
+                        k0 + 8 * ((i - m * chunks) * 32 + lane), p.K);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * W4_WARPS;
       if (i >= items) break;
       const int m = i / chunks, c = i - m * chunks;
-      const uint32_t q[8] = {raw[u][0].x, raw[u][0].y, raw[u][0].z, raw[u][0].w,
-                             raw[u][1].x, raw[u][1].y, raw[u][1].z, raw[u][1].w};
       float v[8], a = W4_TINY;
+      w4_values(raw[u], p.x_f32, v);
       bool fine = true;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        v[e] = p.x_f32 ? __uint_as_float(q[e]) : (e & 1) ? bf16_hi(q[e / 2]) : bf16_lo(q[e / 2]);
         if (p.silu) v[e] = w4_silu(v[e]);
         a = fmaxf(a, fabsf(v[e]));
         fine &= fabsf(v[e]) < INFINITY;
@@ -549,7 +649,7 @@ cudaError_t launch_linear_w4(const W4Params& p, cudaStream_t s) {
   W4Launch L;
   L.p = p;
   L.chunks = (row_bytes + W4_CHUNK / 2 - 1) / (W4_CHUNK / 2);
-  L.x_vec = (reinterpret_cast<uintptr_t>(p.x) & 15) == 0 && p.K % 8 == 0;
+  L.x_vec = w4_vec(p.x, p.K);
   const int passes = (p.M + W4_MAX_ROWS - 1) / W4_MAX_ROWS;
   L.rows_m = (p.M + passes - 1) / passes;
   const int cols = 3 * L.rows_m, nt = (cols + 7) / 8, rows = w4_rows(nt);

@@ -143,8 +143,8 @@ def _check(st: int, where: str):
 
 
 def _stream(stream):
-    if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    if stream is None:  # the current stream's handle, without a Stream object around it (3 us)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
@@ -189,12 +189,12 @@ class _Call:
 
     def dev(self, t, dtype, name: str):
         p = _dev(t, dtype, name)
-        self.devs.append((name, t.device.index))
+        self.devs.append((name, t.get_device()))
         return p
 
     def rows(self, t, dtype, name: str, rows: int, row_stride: int, row_len: int):
         p = _dev_rows(t, dtype, name, rows, row_stride, row_len, self.where)
-        self.devs.append((name, t.device.index))
+        self.devs.append((name, t.get_device()))
         return p
 
     def lens(self, t, n: int, name: str):
@@ -204,8 +204,8 @@ class _Call:
         return p
 
     def check(self):
-        pack = self.w.device if self.w is not None else torch.cuda.current_device()
-        why = device_mismatch(self.devs, torch.cuda.current_device(), pack)
+        current = torch.cuda.current_device()
+        why = device_mismatch(self.devs, current, self.w.device if self.w is not None else current)
         if why:
             raise AFError(AF_ERR_INVALID_ARG, self.where, why)
 
@@ -217,7 +217,7 @@ def _dev(t: torch.Tensor, dtype, name: str):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _need(ok: bool, where: str, detail: str):
@@ -229,8 +229,8 @@ def _need(ok: bool, where: str, detail: str):
 
 
 def _need_shape(t, shape, name: str, where: str):
-    got = tuple(t.shape)
-    _need(got == tuple(shape), where, f"{name} must have shape {tuple(shape)}, got {got}")
+    if t.shape != tuple(shape):
+        raise AFError(AF_ERR_SHAPE, where, f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _elems_from_start(t) -> int:
@@ -246,10 +246,13 @@ def _dev_rows(t, dtype, name: str, rows: int, row_stride: int, row_len: int, whe
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() == 2 and t.stride() == (row_stride, 1) and t.shape[0] >= rows and t.shape[1] >= row_len:
+        return t.data_ptr()  # the view itself spans what the call reads
     need = (rows - 1) * row_stride + row_len if rows > 0 else 0
     avail = _elems_from_start(t)
-    _need(need <= avail, where, f"{name} holds {avail} elements from its start, the call reads {need}")
-    return ctypes.c_void_p(t.data_ptr())
+    if need > avail:
+        raise AFError(AF_ERR_SHAPE, where, f"{name} holds {avail} elements from its start, the call reads {need}")
+    return t.data_ptr()
 
 
 def _width(w) -> int:
@@ -703,18 +706,21 @@ def _w4_args(c: _Call, codes, scales, N: int, K: int, group: int, where: str):
     rows of at least N contiguous entries (a view of wider rows may be given)."""
     want, (groups, _) = w4_shapes(N, K, group)
     _need_shape(codes, want, "codes", where)
-    _need(scales.dim() == 2 and scales.shape[0] == groups and scales.shape[1] >= N, where,
-          f"scales must have shape ({groups}, >= {N}), got {tuple(scales.shape)}")
-    stride = scales.stride(0) if groups > 1 else max(scales.stride(0), (N + 7) // 8 * 8)
-    _need(scales.stride(1) == 1 or scales.shape[1] == 1, where, "scales must be contiguous along their rows")
+    shape = scales.shape
+    if len(shape) != 2 or shape[0] != groups or shape[1] < N:
+        raise AFError(AF_ERR_SHAPE, where, f"scales must have shape ({groups}, >= {N}), got {tuple(shape)}")
+    stride, inner = scales.stride()
+    if groups == 1:
+        stride = max(stride, (N + 7) // 8 * 8)
+    if inner != 1 and shape[1] > 1:
+        raise AFError(AF_ERR_SHAPE, where, "scales must be contiguous along their rows")
     if stride < N or stride % 8 != 0:
         raise AFError(AF_ERR_UNSUPPORTED, where, f"the scales' row stride must be a multiple of 8 and at least {N}, "
                                                  f"got {stride}")
     cp = c.dev(codes, torch.uint8, "codes")
     sp = c.rows(scales, torch.bfloat16, "scales", groups, stride, N)
-    for name, p in (("codes", cp), ("scales", sp)):
-        if (p.value or 0) % 16 != 0:
-            raise AFError(AF_ERR_UNSUPPORTED, where, f"{name} must start on a 16-byte boundary")
+    if (cp | sp) % 16 != 0:
+        raise AFError(AF_ERR_UNSUPPORTED, where, "codes and scales must start on 16-byte boundaries")
     return cp, sp, stride
 
 
@@ -766,30 +772,33 @@ NORMS = {"none": 0, "layer": 1, "rms": 2}
 
 def _residual_norm_args(c: _Call, where, x, branch, x_out, gate, shift, scale, mod_stride, residual_scale, post,
                         post_weight, pre, pre_weight):
-    B, N, D = x.shape
+    B, N, D = shape = x.shape
     dt = _either(x, "x")
     if post not in NORMS or pre not in NORMS:
         raise ValueError(f"post and pre must be one of {sorted(NORMS)}, got {post!r} and {pre!r}")
-    for name, t in (("branch", branch), ("x_out", x_out)):
+
+    for t, name in ((branch, "branch"), (x_out, "x_out")):
         if t is not None:
-            _need_shape(t, (B, N, D), name, where)
-    for name, t in (("post_weight", post_weight), ("pre_weight", pre_weight)):
+            _need_shape(t, shape, name, where)
+    for t, name in ((post_weight, "post_weight"), (pre_weight, "pre_weight")):
         if t is not None:
             _need_shape(t, (D,), name, where)
 
     def opt(t, dtype, name):
         return None if t is None else c.dev(t, dtype, name)
 
-    def vec(t, name):
-        return None if t is None else c.rows(t, torch.float32, name, B, mod_stride, D)
+    def vec(t, name):  # sample b's D values from element b * mod_stride, or None
+        if t is None:
+            return None
+        if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise AFError(AF_ERR_SHAPE, where, f"{name} must be contiguous along its last axis")
+        return c.rows(t, torch.float32, name, B, mod_stride, D)
 
-    for name, t in (("gate", gate), ("shift", shift), ("scale", scale)):
-        if t is not None and t.dim() > 0 and t.shape[-1] > 1:
-            _need(t.stride(-1) == 1, where, f"{name} must be contiguous along its last axis")
-    xp, bp, op = c.dev(x, x.dtype, "x"), opt(branch, x.dtype, "branch"), opt(x_out, x.dtype, "x_out")
-    return (xp, bp, dt, float(residual_scale), vec(gate, "gate"), vec(shift, "shift"), vec(scale, "scale"),
-            mod_stride, NORMS[post], opt(post_weight, torch.float32, "post_weight"), NORMS[pre],
-            opt(pre_weight, torch.float32, "pre_weight"), op)
+    xt = x.dtype
+    return (c.dev(x, xt, "x"), opt(branch, xt, "branch"), dt, float(residual_scale), vec(gate, "gate"),
+            vec(shift, "shift"), vec(scale, "scale"), mod_stride, NORMS[post],
+            opt(post_weight, torch.float32, "post_weight"), NORMS[pre], opt(pre_weight, torch.float32, "pre_weight"),
+            opt(x_out, xt, "x_out"))
 
 
 def residual_norm(x, branch, x_out, y, eps: float, gate=None, shift=None, scale=None, mod_stride: int = 0,
@@ -818,8 +827,10 @@ def residual_norm_e4m3(x, branch, x_out, y8, yscale, eps: float, gate=None, shif
     """residual_norm with y as e4m3 codes y8 (uint8, B * N rows of D) and fp32 row scales yscale."""
     where = "af_residual_norm_e4m3"
     B, N, D = x.shape
-    _need(y8.numel() == B * N * D, where, f"y8 must hold {B * N * D} codes, got {y8.numel()}")
-    _need(yscale.numel() >= B * N, where, f"yscale must hold {B * N} values, got {yscale.numel()}")
+    if y8.numel() != B * N * D:
+        raise AFError(AF_ERR_SHAPE, where, f"y8 must hold {B * N * D} codes, got {y8.numel()}")
+    if yscale.numel() < B * N:
+        raise AFError(AF_ERR_SHAPE, where, f"yscale must hold {B * N} values, got {yscale.numel()}")
     c = _Call(where)
     args = _residual_norm_args(c, where, x, branch, x_out, gate, shift, scale, int(mod_stride), residual_scale, post,
                                post_weight, pre, pre_weight)

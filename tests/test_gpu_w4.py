@@ -99,6 +99,41 @@ def test_quantize_borders(af):
     assert torch.equal(codes, _pack(rc))
 
 
+def test_quantize_every_bf16_quotient(af):
+    """All 128 bf16 significands as the group's maximum, each with every bf16
+    value down to 1/128 of it, both signs: ties and borders bit for bit."""
+    top = (1 + np.arange(128) / 128.0)
+    vals = np.concatenate([top * 2.0 ** -e for e in range(8)])       # 1024 values in [2^-7, 2)
+    rows = []
+    for i, a in enumerate(top):
+        v = vals[vals <= a] * np.where(np.arange(np.sum(vals <= a)) % 2, -1.0, 1.0)
+        v = np.pad(v, (0, -len(v) % 31)).reshape(-1, 31)
+        rows.append(np.concatenate([np.full((len(v), 1), a), v], axis=1) * 2.0 ** (i % 40 - 20))
+    w = np.concatenate(rows).astype(np.float32)
+    N = len(w)
+    cs, ss = af.w4_shapes(N, 32, 32)
+    codes, scales = torch.empty(cs, dtype=torch.uint8, device="cuda"), torch.empty(ss, dtype=BF, device="cuda")
+    rc, rs = O.quantize_rows_w4(w, 32)
+    for dtype in (BF, F32):
+        af.quantize_rows_w4(_dev(w, dtype), 32, codes, scales)
+        assert np.array_equal(scales[:, :N].float().cpu().numpy(), rs)
+        assert torch.equal(codes, _pack(rc))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_quantize_extreme_scales(af, dtype):
+    """Groups from the smallest numbers (no scale, or one of few bits) to the largest."""
+    base = synth.normal(803, "ex", (40, 64), 1.0, "bf16" if dtype == BF else "f32")
+    w = (base.astype(np.float64) * 2.0 ** np.linspace(-149, 125, 40)[:, None]).astype(np.float32)
+    w = synth.bf16_round(w) if dtype == BF else w
+    cs, ss = af.w4_shapes(40, 64, 32)
+    codes, scales = torch.empty(cs, dtype=torch.uint8, device="cuda"), torch.empty(ss, dtype=BF, device="cuda")
+    af.quantize_rows_w4(_dev(w, dtype), 32, codes, scales)
+    rc, rs = O.quantize_rows_w4(w, 32)
+    assert np.array_equal(scales.double().cpu().numpy(), rs)
+    assert torch.equal(codes, _pack(rc))
+
+
 CASES = [  # M, N, K, group, x, out, silu, bias
     (1, 1, 1, 32, F32, F32, False, False), (1, 192, 32, 32, F32, F32, True, False),
     (2, 192, 32, 64, BF, BF, True, True), (3, 17, 31, 32, BF, F32, False, True),

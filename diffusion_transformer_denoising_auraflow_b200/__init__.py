@@ -102,6 +102,7 @@ _SIGS = {
     "af_quantize_rows_e4m3": [_P, _I, _I, _P, _P, _P],
     "af_ln_modulate_e4m3": [_P, _P, _P, _I, _P, _P, _I, _I, _I, _F, _P],
     "af_linear_fp8": [_P, _P, _P, _P, _P, _I, _I, _I, _P],
+    "af_weights_quantize_w4": [_P, _I, _P],
     "af_quantize_rows_w4": [_P, _I, _I, _I, _I, _P, _P, _I, _P],
     "af_dequantize_rows_w4": [_P, _P, _I, _I, _I, _I, _P, _I, _P],
     "af_linear_w4": [_P, _I, _I, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _P],
@@ -349,6 +350,13 @@ class Weights:
         self._check_current("af_weights_quantize_fp8")
         _check(lib.af_weights_quantize_fp8(self.handle, 1 if enable else 0, _stream(stream)),
                "af_weights_quantize_fp8")
+
+    def quantize_w4(self, group: int = 64, stream=None):
+        """Compute every modulation from 4-bit weights with one scale per
+        `group` (32, 64, 128) columns, quantised from the current values, or
+        with group = 0 from the pack's own weights again."""
+        self._check_current("af_weights_quantize_w4")
+        _check(lib.af_weights_quantize_w4(self.handle, int(group), _stream(stream)), "af_weights_quantize_w4")
 
     def nbytes(self) -> int:
         b = ctypes.c_size_t()

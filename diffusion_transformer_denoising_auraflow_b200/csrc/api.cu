@@ -103,6 +103,11 @@ struct af_weights {
   uint8_t* fp8_codes = nullptr;
   float* fp8_scales = nullptr;
   std::unordered_map<std::string, Fp8Region> fp8_region;  // region's first tensor name -> offsets
+  // 4-bit modulations: codes and group scales of the whole adaLN region
+  // (af_weights_quantize_w4); w4_group = 0: off
+  int w4_group = 0, w4_stride = 0;
+  uint8_t* w4_codes = nullptr;
+  uint16_t* w4_scales = nullptr;
 
   const uint16_t* ptr(const std::string& n) const {
     auto it = index.find(n);
@@ -308,6 +313,19 @@ af_status run_gemm(af_scratch* s, const GemmParams& p, const void* A, const void
   cudaError_t e = launch_gemm(p, A, W, W_rows, st, s->sms);
   if (e != cudaSuccess) return cuda_fail(e);
   return AF_OK;
+}
+
+// out[b, r] = W_ada[row0 + r] . silu(temb[b]) with the 4-bit modulation weights.
+// Accounted by the weight stream: half a byte a weight and a scale per group.
+af_status modulation_w4(const af_weights* w, af_scratch* s, const float* temb, int B, size_t row0, int rows,
+                        float* out, cudaStream_t st) {
+  const int D = w->d.D, g = w->w4_group, groups = (D + g - 1) / g;
+  LaunchScope ls(s, KC_OTHER, rows * (groups * (g / 2.0 + 2.0)), st);
+  W4Params p{temb, w->w4_codes + row0 * groups * (g / 2), w->w4_scales + row0, nullptr, out,
+             B,    rows, D, g, w->w4_stride, rows, 1, 1, 1};
+  p.err = s->err;
+  const cudaError_t e = launch_linear_w4(p, st);
+  return e == cudaSuccess ? AF_OK : cuda_fail(e);
 }
 
 // A GEMM operand: bf16 (scale == nullptr) or e4m3 codes with one fp32 scale per row.
@@ -675,6 +693,7 @@ af_status f32_timestep_mlp(const af_weights* w, F32Step& k, const float* t, int 
 
 af_status f32_modulations(const af_weights* w, F32Step& k, const float* temb, int B, float* out) {
   const int rows = static_cast<int>(w->ada_rows);
+  if (w->w4_group) return modulation_w4(w, k.s, temb, B, 0, rows, out, k.st);
   LaunchScope ls(k.s, KC_OTHER, 4.0 * rows * w->d.D, k.st);
   return f32_done(f32_gemv(temb, B, w->d.D, reinterpret_cast<const float*>(w->base + w->tensors[0].offset), nullptr,
                            rows, 1, 0, out, rows, k.st));
@@ -875,6 +894,8 @@ void af_weights_destroy(af_weights* w) {
   if (w->base) cudaFree(w->base);
   if (w->fp8_codes) cudaFree(w->fp8_codes);
   if (w->fp8_scales) cudaFree(w->fp8_scales);
+  if (w->w4_codes) cudaFree(w->w4_codes);
+  if (w->w4_scales) cudaFree(w->w4_scales);
   delete w;
 }
 
@@ -1073,6 +1094,38 @@ af_status af_weights_quantize_fp8(af_weights* w, int enable, void* stream) {
   return AF_OK;
 }
 
+af_status af_weights_quantize_w4(af_weights* w, int group, void* stream) {
+  if (!w) return AF_ERR_INVALID_ARG;
+  if (!(group == 0 || group == 32 || group == 64 || group == 128)) return AF_ERR_UNSUPPORTED;
+  AF_TRY(check_device(w));
+  if (group != w->w4_group) {
+    if (w->w4_codes) cudaFree(w->w4_codes);
+    if (w->w4_scales) cudaFree(w->w4_scales);
+    w->w4_codes = nullptr;
+    w->w4_scales = nullptr;
+    w->w4_group = 0;
+  }
+  if (group == 0) return AF_OK;
+  const int rows = static_cast<int>(w->ada_rows), D = w->d.D, groups = (D + group - 1) / group;
+  const int stride = (rows + 7) / 8 * 8;
+  if (!w->w4_codes) {
+    cudaError_t e = cudaMalloc(&w->w4_codes, static_cast<size_t>(rows) * groups * (group / 2));
+    if (e == cudaSuccess) e = cudaMalloc(&w->w4_scales, static_cast<size_t>(groups) * stride * 2);
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      if (w->w4_codes) cudaFree(w->w4_codes);
+      w->w4_codes = nullptr;
+      w->w4_scales = nullptr;
+      return AF_ERR_OOM;
+    }
+  }
+  AF_CUDA(launch_quantize_rows_w4(w->base + w->tensors[0].offset, w->f32, rows, D, group, w->w4_codes, w->w4_scales,
+                                  stride, static_cast<cudaStream_t>(stream)));
+  w->w4_group = group;
+  w->w4_stride = stride;
+  return AF_OK;
+}
+
 af_status af_weights_bytes(const af_weights* w, size_t* bytes) {
   if (!w || !bytes) return AF_ERR_INVALID_ARG;
   *bytes = w->bytes;
@@ -1247,10 +1300,11 @@ af_status af_joint_block(const af_weights* w, af_scratch* s, int layer, uint16_t
   const int D = w->d.D;
   // modulation of this block's two streams only
   const size_t r_img = w->unit_row[2 * layer];
-  const uint16_t* ada = ada_base(w);
-  {
+  if (w->w4_group) {
+    AF_TRY(modulation_w4(w, s, temb, B, r_img, 12 * D, s->mods, st));
+  } else {
     LaunchScope ls(s, KC_OTHER, 2.0 * 12 * D * D, st, (B + 7) / 8);
-    AF_CUDA(launch_modulation(temb, B, D, ada + r_img * D, 12 * D, s->mods, st));
+    AF_CUDA(launch_modulation(temb, B, D, ada_base(w) + r_img * D, 12 * D, s->mods, st));
   }
   const float* mi = s->mods;
   const float* mt = s->mods + 6 * D;
@@ -1268,7 +1322,9 @@ af_status af_single_block(const af_weights* w, af_scratch* s, int layer, uint16_
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int D = w->d.D;
   const size_t r = w->unit_row[2 * w->cfg.num_mmdit_layers + layer];
-  {
+  if (w->w4_group) {
+    AF_TRY(modulation_w4(w, s, temb, B, r, 6 * D, s->mods, st));
+  } else {
     LaunchScope ls(s, KC_OTHER, 2.0 * 6 * D * D, st, (B + 7) / 8);
     AF_CUDA(launch_modulation(temb, B, D, ada_base(w) + r * D, 6 * D, s->mods, st));
   }
@@ -1345,7 +1401,9 @@ static af_status forward_impl(const af_weights* w, af_scratch* s, const float* l
                                 w->ptr("time_step_proj.linear_2.bias"), c.timestep_channels, D, s->tfeat, s->h1,
                                 s->temb, st));
   }
-  if (!premods) {
+  if (!premods && w->w4_group) {
+    AF_TRY(modulation_w4(w, s, s->temb, B, 0, static_cast<int>(R_ada), s->mods, st));
+  } else if (!premods) {
     // every modulation of the step in one tensor-core GEMM over the adaLN
     // rows (mods[b, r] = W_ada[r] . silu(temb_b)), silu(temb) rounded to bf16
     // as in the sampler plan: the 4.6 GB of modulation weights stream once at
@@ -1547,6 +1605,7 @@ af_status af_sampler_prepare(af_sampler* m, void* stream) {
                                 w->ptr("time_step_proj.linear_1.bias"), w->ptr("time_step_proj.linear_2.weight"),
                                 w->ptr("time_step_proj.linear_2.bias"), C, D, m->feat, m->h1, m->temb, st));
   }
+  if (w->w4_group) return modulation_w4(w, s, m->temb, n, 0, static_cast<int>(w->ada_rows), m->mods, st);
   {
     LaunchScope ls(s, KC_OTHER, 6.0 * n * D, st);
     AF_CUDA(launch_silu_bf16(m->temb, n * D, m->silu, st));

@@ -147,7 +147,7 @@ af_status af_weights_get(const af_weights* w, int id, void* dst, int dst_is_devi
  * words become uniforms (x + 1/2) / 2^32 and the Box-Muller transform (in
  * fp64) turns pairs into normals; the stored value is float32(z * std),
  * rounded to bf16 (nearest even) in a bf16 pack.  Asynchronous on `stream`.
- * An 8-bit copy made by af_weights_quantize_fp8 is not refreshed. */
+ * Copies made by af_weights_quantize_fp8 and _w4 are not refreshed. */
 af_status af_weights_init_random(af_weights* w, uint64_t seed, float std, void* stream);
 /* Total bytes of the pack (for reporting). */
 af_status af_weights_bytes(const af_weights* w, size_t* bytes);
@@ -420,6 +420,17 @@ af_status af_dequantize_rows_w4(const uint8_t* codes, const uint16_t* scales, in
 af_status af_linear_w4(const void* x, int x_dtype, int silu, const uint8_t* codes, const uint16_t* scales,
                        int scale_stride, const float* bias, void* out, int out_dtype, int M, int N, int K, int group,
                        void* stream);
+
+/* Keep the modulation weights of a pack (every adaLN-Zero linear and the
+ * pre-final one, a third of the model's parameters) in 4 bits: quantises their
+ * current values into a second device copy (af_quantize_rows_w4 with `group`)
+ * and makes every later block, forward, denoise step and af_sampler_prepare
+ * on `w` compute its modulations from it with af_linear_w4 (silu(temb) in
+ * fp32).  bf16 and fp32 packs, with or without the 8-bit projections.  Call it
+ * again after changing weights; group = 0 frees the copy and returns to the
+ * pack's own weights.  Work on `w` in flight must have ended when the copy is
+ * freed or re-made with another group. */
+af_status af_weights_quantize_w4(af_weights* w, int group, void* stream);
 
 /* Host-side sigma schedule of the flow-match Euler sampler ([DEEP] §2.3:
  * num_train_timesteps 1000, shift 1.73, 25 steps): n_steps + 1 values

@@ -690,15 +690,55 @@ def linear_fp8(A8, a_scale, W8, w_scale, C, stream=None):
 
 
 # ---- 4-bit weights, and the residual between two norms
+#
+# Calls of a few microseconds on the device: a tensor that is as it should be
+# costs one condition here, the messages are made where one is not.
 
 _DTYPE_CODE = {torch.bfloat16: AF_DTYPE_BF16, torch.float32: AF_DTYPE_F32}
 
 
-def _either(t, name: str):
+def _dtype_code(t, name: str) -> int:
     """The AF_DTYPE code of a tensor that may be bf16 or fp32."""
-    if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPE_CODE:
+    code = _DTYPE_CODE.get(getattr(t, "dtype", None))
+    if code is None:
         raise TypeError(f"{name} must be a bfloat16 or float32 tensor")
-    return _DTYPE_CODE[t.dtype]
+    return code
+
+
+def _current(t) -> int:
+    """The current device, or for a CPU tensor a number that no tensor's device has."""
+    return torch.cuda.current_device() if t.is_cuda else -2
+
+
+def _on_device(t, name: str, where: str, dev: int):
+    if t.get_device() != dev:
+        why = device_mismatch([(name, t.get_device())], dev, dev)
+        raise AFError(AF_ERR_INVALID_ARG, where, why)
+    return t.data_ptr()
+
+
+def _ptr(t, dtype, name: str, where: str, dev: int):
+    """Address of a contiguous tensor of `dtype` on the current device `dev`; None for None."""
+    if t is None:
+        return None
+    if t.get_device() == dev and t.dtype == dtype and t.is_contiguous():
+        return t.data_ptr()
+    _dev(t, dtype, name)
+    return _on_device(t, name, where, dev)
+
+
+def _ptr_rows(t, dtype, name: str, where: str, dev: int, rows: int, row_stride: int, row_len: int):
+    """The same for a view read as `rows` rows of `row_len` elements, `row_stride` apart; None for None."""
+    if t is None:
+        return None
+    if t.get_device() == dev and t.dtype == dtype and t.dim() == 2 and t.stride() == (row_stride, 1):
+        n, m = t.shape
+        if n >= rows and m >= row_len:
+            return t.data_ptr()
+    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise AFError(AF_ERR_SHAPE, where, f"{name} must be contiguous along its last axis")
+    _dev_rows(t, dtype, name, rows, row_stride, row_len, where)
+    return _on_device(t, name, where, dev)
 
 
 def w4_shapes(N: int, K: int, group: int):
@@ -709,25 +749,22 @@ def w4_shapes(N: int, K: int, group: int):
     return (N, groups * group // 2), (groups, (N + 7) // 8 * 8)
 
 
-def _w4_args(c: _Call, codes, scales, N: int, K: int, group: int, where: str):
+def _w4_args(codes, scales, N: int, K: int, group: int, where: str, dev: int):
     """Pointers and scale stride of a 4-bit weight: codes contiguous, scales
     rows of at least N contiguous entries (a view of wider rows may be given)."""
-    want, (groups, _) = w4_shapes(N, K, group)
-    _need_shape(codes, want, "codes", where)
+    want, (groups, padded) = w4_shapes(N, K, group)
+    if codes.shape != want:
+        _need_shape(codes, want, "codes", where)
     shape = scales.shape
     if len(shape) != 2 or shape[0] != groups or shape[1] < N:
         raise AFError(AF_ERR_SHAPE, where, f"scales must have shape ({groups}, >= {N}), got {tuple(shape)}")
-    stride, inner = scales.stride()
-    if groups == 1:
-        stride = max(stride, (N + 7) // 8 * 8)
-    if inner != 1 and shape[1] > 1:
-        raise AFError(AF_ERR_SHAPE, where, "scales must be contiguous along their rows")
+    stride = scales.stride(0) if groups > 1 else max(scales.stride(0), padded)
     if stride < N or stride % 8 != 0:
-        raise AFError(AF_ERR_UNSUPPORTED, where, f"the scales' row stride must be a multiple of 8 and at least {N}, "
-                                                 f"got {stride}")
-    cp = c.dev(codes, torch.uint8, "codes")
-    sp = c.rows(scales, torch.bfloat16, "scales", groups, stride, N)
-    if (cp | sp) % 16 != 0:
+        raise AFError(AF_ERR_UNSUPPORTED if scales.stride(1) == 1 else AF_ERR_SHAPE, where,
+                      f"the scales' row stride must be a multiple of 8 and at least {N}, got {stride}")
+    cp = _ptr(codes, torch.uint8, "codes", where, dev)
+    sp = _ptr_rows(scales, torch.bfloat16, "scales", where, dev, groups, stride, N)
+    if (cp | sp) & 15:
         raise AFError(AF_ERR_UNSUPPORTED, where, "codes and scales must start on 16-byte boundaries")
     return cp, sp, stride
 
@@ -736,24 +773,26 @@ def quantize_rows_w4(w, group: int, codes, scales, stream=None):
     """4-bit codes and group scales of w [N, K] (bf16 or fp32) into codes and scales (shapes: w4_shapes)."""
     where = "af_quantize_rows_w4"
     N, K = w.shape
-    dt = _either(w, "w")
-    c = _Call(where)
-    cp, sp, stride = _w4_args(c, codes, scales, N, K, group, where)
-    wp = c.dev(w, w.dtype, "w")
-    c.check()
-    _check(lib.af_quantize_rows_w4(wp, dt, N, K, group, cp, sp, stride, _stream(stream)), where)
+    dt = _dtype_code(w, "w")
+    dev = _current(w)
+    cp, sp, stride = _w4_args(codes, scales, N, K, group, where, dev)
+    wp = _ptr(w, w.dtype, "w", where, dev)
+    st = lib.af_quantize_rows_w4(wp, dt, N, K, group, cp, sp, stride, _stream(stream))
+    if st:
+        _check(st, where)
 
 
 def dequantize_rows_w4(codes, scales, group: int, out, stream=None):
     """The values of 4-bit codes and scales into out [N, K] (bf16 or fp32)."""
     where = "af_dequantize_rows_w4"
     N, K = out.shape
-    dt = _either(out, "out")
-    c = _Call(where)
-    cp, sp, stride = _w4_args(c, codes, scales, N, K, group, where)
-    op = c.dev(out, out.dtype, "out")
-    c.check()
-    _check(lib.af_dequantize_rows_w4(cp, sp, stride, N, K, group, op, dt, _stream(stream)), where)
+    dt = _dtype_code(out, "out")
+    dev = _current(out)
+    cp, sp, stride = _w4_args(codes, scales, N, K, group, where, dev)
+    op = _ptr(out, out.dtype, "out", where, dev)
+    st = lib.af_dequantize_rows_w4(cp, sp, stride, N, K, group, op, dt, _stream(stream))
+    if st:
+        _check(st, where)
 
 
 def linear_w4(x, codes, scales, group: int, out, silu: bool = False, bias=None, stream=None):
@@ -762,51 +801,43 @@ def linear_w4(x, codes, scales, group: int, out, silu: bool = False, bias=None, 
     where = "af_linear_w4"
     M, K = x.shape
     N = codes.shape[0]
-    _need_shape(out, (M, N), "out", where)
-    xt, ot = _either(x, "x"), _either(out, "out")
+    if out.shape != (M, N):
+        _need_shape(out, (M, N), "out", where)
     if bias is not None:
         _need_shape(bias, (N,), "bias", where)
-    c = _Call(where)
-    cp, sp, stride = _w4_args(c, codes, scales, N, K, group, where)
-    xp, op = c.dev(x, x.dtype, "x"), c.dev(out, out.dtype, "out")
-    bp = c.dev(bias, torch.float32, "bias") if bias is not None else None
-    c.check()
-    _check(lib.af_linear_w4(xp, xt, 1 if silu else 0, cp, sp, stride, bp, op, ot, M, N, K, group, _stream(stream)),
-           where)
+    xt, ot = _dtype_code(x, "x"), _dtype_code(out, "out")
+    dev = _current(x)
+    cp, sp, stride = _w4_args(codes, scales, N, K, group, where, dev)
+    st = lib.af_linear_w4(_ptr(x, x.dtype, "x", where, dev), xt, 1 if silu else 0, cp, sp, stride,
+                          _ptr(bias, torch.float32, "bias", where, dev), _ptr(out, out.dtype, "out", where, dev), ot,
+                          M, N, K, group, _stream(stream))
+    if st:
+        _check(st, where)
 
 
 NORMS = {"none": 0, "layer": 1, "rms": 2}
 
 
-def _residual_norm_args(c: _Call, where, x, branch, x_out, gate, shift, scale, mod_stride, residual_scale, post,
-                        post_weight, pre, pre_weight):
-    B, N, D = shape = x.shape
-    dt = _either(x, "x")
+def _residual_norm_args(where, x, branch, x_out, gate, shift, scale, mod_stride, residual_scale, post, post_weight, pre,
+                        pre_weight, dev):
+    B, _, D = shape = x.shape
     if post not in NORMS or pre not in NORMS:
         raise ValueError(f"post and pre must be one of {sorted(NORMS)}, got {post!r} and {pre!r}")
-
-    for t, name in ((branch, "branch"), (x_out, "x_out")):
-        if t is not None:
-            _need_shape(t, shape, name, where)
-    for t, name in ((post_weight, "post_weight"), (pre_weight, "pre_weight")):
-        if t is not None:
-            _need_shape(t, (D,), name, where)
-
-    def opt(t, dtype, name):
-        return None if t is None else c.dev(t, dtype, name)
-
-    def vec(t, name):  # sample b's D values from element b * mod_stride, or None
-        if t is None:
-            return None
-        if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
-            raise AFError(AF_ERR_SHAPE, where, f"{name} must be contiguous along its last axis")
-        return c.rows(t, torch.float32, name, B, mod_stride, D)
-
-    xt = x.dtype
-    return (c.dev(x, xt, "x"), opt(branch, xt, "branch"), dt, float(residual_scale), vec(gate, "gate"),
-            vec(shift, "shift"), vec(scale, "scale"), mod_stride, NORMS[post],
-            opt(post_weight, torch.float32, "post_weight"), NORMS[pre], opt(pre_weight, torch.float32, "pre_weight"),
-            opt(x_out, xt, "x_out"))
+    if branch is not None and branch.shape != shape:
+        _need_shape(branch, shape, "branch", where)
+    if x_out is not None and x_out.shape != shape:
+        _need_shape(x_out, shape, "x_out", where)
+    if post_weight is not None:
+        _need_shape(post_weight, (D,), "post_weight", where)
+    if pre_weight is not None:
+        _need_shape(pre_weight, (D,), "pre_weight", where)
+    xt, f32 = x.dtype, torch.float32
+    return (_ptr(x, xt, "x", where, dev), _ptr(branch, xt, "branch", where, dev), _DTYPE_CODE[xt], residual_scale,
+            _ptr_rows(gate, f32, "gate", where, dev, B, mod_stride, D),
+            _ptr_rows(shift, f32, "shift", where, dev, B, mod_stride, D),
+            _ptr_rows(scale, f32, "scale", where, dev, B, mod_stride, D), mod_stride, NORMS[post],
+            _ptr(post_weight, f32, "post_weight", where, dev), NORMS[pre],
+            _ptr(pre_weight, f32, "pre_weight", where, dev), _ptr(x_out, xt, "x_out", where, dev))
 
 
 def residual_norm(x, branch, x_out, y, eps: float, gate=None, shift=None, scale=None, mod_stride: int = 0,
@@ -819,14 +850,15 @@ def residual_norm(x, branch, x_out, y, eps: float, gate=None, shift=None, scale=
     branch, x_out or y may be None (see af_residual_norm)."""
     where = "af_residual_norm"
     B, N, D = x.shape
-    if y is not None:
+    _dtype_code(x, "x")
+    if y is not None and y.shape != x.shape:
         _need_shape(y, (B, N, D), "y", where)
-    c = _Call(where)
-    args = _residual_norm_args(c, where, x, branch, x_out, gate, shift, scale, int(mod_stride), residual_scale, post,
-                               post_weight, pre, pre_weight)
-    yp = None if y is None else c.dev(y, x.dtype, "y")
-    c.check()
-    _check(lib.af_residual_norm(*args, yp, B, N, D, float(eps), _stream(stream)), where)
+    dev = _current(x)
+    args = _residual_norm_args(where, x, branch, x_out, gate, shift, scale, mod_stride, residual_scale, post,
+                               post_weight, pre, pre_weight, dev)
+    st = lib.af_residual_norm(*args, _ptr(y, x.dtype, "y", where, dev), B, N, D, eps, _stream(stream))
+    if st:
+        _check(st, where)
 
 
 def residual_norm_e4m3(x, branch, x_out, y8, yscale, eps: float, gate=None, shift=None, scale=None,
@@ -835,16 +867,18 @@ def residual_norm_e4m3(x, branch, x_out, y8, yscale, eps: float, gate=None, shif
     """residual_norm with y as e4m3 codes y8 (uint8, B * N rows of D) and fp32 row scales yscale."""
     where = "af_residual_norm_e4m3"
     B, N, D = x.shape
+    _dtype_code(x, "x")
     if y8.numel() != B * N * D:
         raise AFError(AF_ERR_SHAPE, where, f"y8 must hold {B * N * D} codes, got {y8.numel()}")
     if yscale.numel() < B * N:
         raise AFError(AF_ERR_SHAPE, where, f"yscale must hold {B * N} values, got {yscale.numel()}")
-    c = _Call(where)
-    args = _residual_norm_args(c, where, x, branch, x_out, gate, shift, scale, int(mod_stride), residual_scale, post,
-                               post_weight, pre, pre_weight)
-    yp, sp = c.dev(y8, torch.uint8, "y8"), c.dev(yscale, torch.float32, "yscale")
-    c.check()
-    _check(lib.af_residual_norm_e4m3(*args, yp, sp, B, N, D, float(eps), _stream(stream)), where)
+    dev = _current(x)
+    args = _residual_norm_args(where, x, branch, x_out, gate, shift, scale, mod_stride, residual_scale, post,
+                               post_weight, pre, pre_weight, dev)
+    st = lib.af_residual_norm_e4m3(*args, _ptr(y8, torch.uint8, "y8", where, dev),
+                                   _ptr(yscale, torch.float32, "yscale", where, dev), B, N, D, eps, _stream(stream))
+    if st:
+        _check(st, where)
 
 
 AF_IPC_HANDLE_BYTES = 64

@@ -15,48 +15,6 @@ namespace af {
 
 namespace {
 
-constexpr int RN_THREADS = 256;
-
-// Sum of v over the block, to every thread.
-__device__ __forceinline__ float rn_block_sum(float v, float* red) {
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();  // the last call's values are read
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0.f;
-#pragma unroll
-  for (int i = 0; i < RN_THREADS / 32; ++i) v += red[i];
-  return v;
-}
-__device__ __forceinline__ float rn_block_max(float v, float* red) {
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = red[0];
-#pragma unroll
-  for (int i = 1; i < RN_THREADS / 32; ++i) v = fmaxf(v, red[i]);
-  return v;
-}
-
-// (mean, 1 / root) of the row that this thread holds every RN_THREADS-th
-// value of (each thread reads only what it wrote).
-__device__ __forceinline__ float2 rn_stats(const float* row, int D, int kind, float eps, float* red) {
-  if (kind == NORM_NONE) return make_float2(0.f, 1.f);
-  float mean = 0.f;
-  if (kind == NORM_LAYER) {
-    float s = 0.f;
-    for (int d = threadIdx.x; d < D; d += RN_THREADS) s += row[d];
-    mean = rn_block_sum(s, red) / D;
-  }
-  float q = 0.f;
-  for (int d = threadIdx.x; d < D; d += RN_THREADS) {
-    const float c = row[d] - mean;
-    q += c * c;
-  }
-  return make_float2(mean, rsqrtf(rn_block_sum(q, red) / D + eps));
-}
-
 template <typename T>
 __device__ __forceinline__ float rn_load(const void* p, size_t i) {
   if constexpr (sizeof(T) == 4) return static_cast<const float*>(p)[i];
@@ -68,50 +26,124 @@ __device__ __forceinline__ void rn_store(void* p, size_t i, float v) {
   else static_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(pack_bf16(v, 0.f));
 }
 
-// One CTA per row, the row in shared memory as fp32; any width and alignment.
-template <typename T, bool OUT8>
-__global__ void __launch_bounds__(RN_THREADS) residual_norm_row_kernel(ResidualNormParams p) {
-  extern __shared__ float row[];
-  __shared__ float red[RN_THREADS / 32];
-  const int D = p.D;
-  const size_t r = blockIdx.x, base = r * D;
-  const size_t mo = r / p.rows_per_batch * static_cast<size_t>(p.mod_stride);
-  if (p.branch) {
-    for (int d = threadIdx.x; d < D; d += RN_THREADS) row[d] = rn_load<T>(p.branch, base + d);
-    const float2 st = rn_stats(row, D, p.post, p.eps, red);
-    for (int d = threadIdx.x; d < D; d += RN_THREADS) {
-      float u = (row[d] - st.x) * st.y;
-      if (p.post_weight) u *= p.post_weight[d];
-      if (p.gate) u *= p.gate[mo + d];
-      row[d] = rn_load<T>(p.x, base + d) + p.residual_scale * u;
+// ------------------------------------------------------------------ any width and alignment
+// TG threads per row, E columns a thread in registers, one load or store per
+// value.  Up to 128 columns TG is a power of two within a warp, the columns TG
+// apart, and a CTA takes 256 / TG rows; wider rows take whole warps, each E times
+// 32 neighbouring columns (constant offsets), and above a warp a CTA each.
+constexpr int RN_THREADS = 256;
+
+template <typename T, bool OUT8, int E, bool WIDE>
+__global__ void __launch_bounds__(1024)
+    residual_norm_any_kernel(const __grid_constant__ ResidualNormParams p, int tg) {
+  __shared__ float red[2][32];
+  const int tid = tg > 32 ? threadIdx.x : threadIdx.x & (tg - 1), D = p.D;
+  const int c0 = WIDE ? (tid >> 5) * (32 * E) + (tid & 31) : tid, step = WIDE ? 32 : tg;
+  const int64_t rows = static_cast<int64_t>(p.B) * p.rows_per_batch;
+  const int64_t r = tg > 32 ? blockIdx.x : (static_cast<int64_t>(blockIdx.x) * RN_THREADS + threadIdx.x) / tg;
+  const bool live = r < rows;
+  const size_t base = static_cast<size_t>(live ? r : rows - 1) * D;  // lanes behind the last row repeat it
+  const size_t mo = static_cast<size_t>((live ? r : rows - 1) / p.rows_per_batch) * p.mod_stride;
+  const float inv_d = 1.0f / static_cast<float>(D);
+  int buf = 0;
+  auto join = [&](float v, bool max) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      if (o < tg) {
+        const float t = __shfl_xor_sync(0xffffffffu, v, o);
+        v = max ? fmaxf(v, t) : v + t;
+      }
+    if (tg <= 32) return v;
+    float* w = red[buf];  // two buffers in turn: one barrier per sum
+    buf ^= 1;
+    if ((threadIdx.x & 31) == 0) w[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = w[0];
+    for (int i = 1; i < tg >> 5; ++i) v = max ? fmaxf(v, w[i]) : v + w[i];
+    return v;
+  };
+  auto normalise = [&](float (&v)[E], int kind) {
+    if (kind == NORM_NONE) return;
+    float mean = 0.f, q = 0.f;
+    if (kind == NORM_LAYER) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) mean += v[i];  // zero behind D
+      mean = join(mean, false) * inv_d;
     }
-  } else {
-    for (int d = threadIdx.x; d < D; d += RN_THREADS) row[d] = rn_load<T>(p.x, base + d);
-  }
-  if (p.x_out)
-    for (int d = threadIdx.x; d < D; d += RN_THREADS) rn_store<T>(p.x_out, base + d, row[d]);
-  if (!p.y) return;
-  const float2 st = rn_stats(row, D, p.pre, p.eps, red);
-  float amax = 0.f;
-  for (int d = threadIdx.x; d < D; d += RN_THREADS) {
-    float y = (row[d] - st.x) * st.y;
-    if (p.pre_weight) y *= p.pre_weight[d];
-    if (p.scale) y *= 1.0f + p.scale[mo + d];
-    if (p.shift) y += p.shift[mo + d];
-    if constexpr (OUT8) {
-      row[d] = y;
-      amax = fmaxf(amax, fabsf(y));
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if (c0 + i * step < D) {
+        v[i] -= mean;
+        q += v[i] * v[i];
+      }
+    const float f = rsqrtf(join(q, false) * inv_d + p.eps);
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] *= f;
+  };
+  // everything the row needs is asked for at once, before any of it is used
+  auto load = [&](const float* f, size_t at, float none, float (&v)[E]) {
+    if (f) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[i] = c0 + i * step < D ? __ldg(f + at + c0 + i * step) : none;
     } else {
-      rn_store<T>(p.y, base + d, y);
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[i] = none;
     }
+  };
+  auto load_row = [&](const void* t, float (&v)[E]) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = c0 + i * step < D ? rn_load<T>(t, base + c0 + i * step) : 0.f;
+  };
+  float x[E], u[E], fg[E], fa[E], fs[E];
+  load_row(p.x, x);
+  if (p.branch) load_row(p.branch, u);
+  load(p.gate, mo, 1.f, fg);
+  load(p.scale, mo, 0.f, fa);
+  load(p.shift, mo, 0.f, fs);
+  if (p.post_weight) {
+    float w[E];
+    load(p.post_weight, 0, 0.f, w);
+#pragma unroll
+    for (int i = 0; i < E; ++i) fg[i] *= w[i];
+  }
+#pragma unroll
+  for (int i = 0; i < E; ++i) fa[i] += 1.f;
+  if (p.pre_weight) {
+    float w[E];
+    load(p.pre_weight, 0, 0.f, w);
+#pragma unroll
+    for (int i = 0; i < E; ++i) fa[i] *= w[i];
+  }
+  if (p.branch) {
+    normalise(u, p.post);
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[i] += p.residual_scale * fg[i] * u[i];
+  }
+  if (p.x_out && live) {
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if (c0 + i * step < D) rn_store<T>(p.x_out, base + c0 + i * step, x[i]);
+  }
+  if (!p.y) return;
+  normalise(x, p.pre);
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const int d = c0 + i * step;
+    if (d >= D) continue;
+    x[i] = x[i] * fa[i] + fs[i];
+    if constexpr (OUT8) amax = fmaxf(amax, fabsf(x[i]));
+    else if (live) rn_store<T>(p.y, base + d, x[i]);
   }
   if constexpr (OUT8) {
-    amax = rn_block_max(amax, red);
+    amax = join(amax, true);
     const float inv = amax > 0.f ? 448.0f / amax : 1.0f;
-    uint8_t* y8 = static_cast<uint8_t*>(p.y) + base;
-    for (int d = threadIdx.x; d < D; d += RN_THREADS)
-      y8[d] = static_cast<uint8_t>(pack_e4m3x4(row[d] * inv, 0.f, 0.f, 0.f));
-    if (threadIdx.x == 0) p.yscale[r] = amax > 0.f ? amax / 448.0f : 1.0f;
+    if (!live) return;
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if (c0 + i * step < D)
+        static_cast<uint8_t*>(p.y)[base + c0 + i * step] = static_cast<uint8_t>(pack_e4m3x4(x[i] * inv, 0.f, 0.f, 0.f));
+    if (tid == 0) p.yscale[r] = amax > 0.f ? amax / 448.0f : 1.0f;
   }
 }
 
@@ -232,17 +264,17 @@ __global__ void __launch_bounds__(RING ? RN_RING_THREADS : 512, V == 1 ? 2 : 1)
   const size_t mo = static_cast<size_t>(b) * p.mod_stride;
   auto gate_of = [&](int d) {
     float f = p.residual_scale;
-    if (p.gate) f *= p.gate[mo + d];
-    if (p.post_weight) f *= p.post_weight[d];
+    if (p.gate) f *= __ldg(p.gate + mo + d);
+    if (p.post_weight) f *= __ldg(p.post_weight + d);
     return f;
   };
   auto mul_of = [&](int d) {
     float f = 1.f;
-    if (p.scale) f += p.scale[mo + d];
-    if (p.pre_weight) f *= p.pre_weight[d];
+    if (p.scale) f += __ldg(p.scale + mo + d);
+    if (p.pre_weight) f *= __ldg(p.pre_weight + d);
     return f;
   };
-  auto add_of = [&](int d) { return p.shift ? p.shift[mo + d] : 0.f; };
+  auto add_of = [&](int d) { return p.shift ? __ldg(p.shift + mo + d) : 0.f; };
   // eight columns of the factors from column c
   auto eight = [&](int which, int c, uint64_t (&f)[4]) {
     if (plan.staged) {
@@ -564,25 +596,35 @@ static cudaError_t rn_launch(const ResidualNormParams& p, cudaStream_t s) {
   return cudaErrorInvalidValue;
 }
 
+template <typename T, bool OUT8>
+static cudaError_t rn_any(const ResidualNormParams& p, cudaStream_t s) {
+  const size_t rows = static_cast<size_t>(p.B) * p.rows_per_batch;
+  int tg = 4, threads = RN_THREADS;
+  if (p.D <= 128) {  // four columns a thread
+    while (tg < 32 && tg * 4 < p.D) tg *= 2;
+  } else {  // eight, sixteen above 8192
+    tg = (p.D + 255) / 256 * 32;
+    if (tg > 1024) tg = 1024;
+    if (tg > 32) threads = tg;
+  }
+  const int e = (p.D + tg - 1) / tg;
+  const unsigned grid = static_cast<unsigned>((rows * tg + threads - 1) / threads);
+  auto kernel = p.D <= 128 ? residual_norm_any_kernel<T, OUT8, 4, false>
+                : e <= 8   ? residual_norm_any_kernel<T, OUT8, 8, true>
+                           : residual_norm_any_kernel<T, OUT8, 16, true>;
+  kernel<<<grid, threads, 0, s>>>(p, tg);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_residual_norm(const ResidualNormParams& p, bool f32, cudaStream_t s) {
   auto al = [](const void* a) { return (reinterpret_cast<uintptr_t>(a) & 15) == 0; };
-  if (p.D % 8 == 0 && al(p.x) && al(p.branch) && al(p.x_out) && al(p.y)) {
-    if (p.yscale) return f32 ? rn_launch<float, true>(p, s) : rn_launch<uint16_t, true>(p, s);
-    return f32 ? rn_launch<float, false>(p, s) : rn_launch<uint16_t, false>(p, s);
+  const bool vec = p.D % 8 == 0 && al(p.x) && al(p.branch) && al(p.x_out) && al(p.y);
+  if (p.yscale) {
+    if (vec) return f32 ? rn_launch<float, true>(p, s) : rn_launch<uint16_t, true>(p, s);
+    return f32 ? rn_any<float, true>(p, s) : rn_any<uint16_t, true>(p, s);
   }
-  const size_t rows = static_cast<size_t>(p.B) * p.rows_per_batch;
-  const size_t smem = static_cast<size_t>(p.D) * sizeof(float);
-  auto launch = [&](auto kernel) {
-    if (smem > 48 * 1024) {
-      const cudaError_t e =
-          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-      if (e != cudaSuccess) return e;
-    }
-    kernel<<<static_cast<unsigned>(rows), RN_THREADS, smem, s>>>(p);
-    return cudaGetLastError();
-  };
-  if (p.yscale) return f32 ? launch(residual_norm_row_kernel<float, true>) : launch(residual_norm_row_kernel<uint16_t, true>);
-  return f32 ? launch(residual_norm_row_kernel<float, false>) : launch(residual_norm_row_kernel<uint16_t, false>);
+  if (vec) return f32 ? rn_launch<float, false>(p, s) : rn_launch<uint16_t, false>(p, s);
+  return f32 ? rn_any<float, false>(p, s) : rn_any<uint16_t, false>(p, s);
 }
 
 }  // namespace af

@@ -119,7 +119,8 @@ def test_matches_oracle(af, B, N, D, dtype, post, pre, gate, mod, pw, qw, r):
 
 @pytest.mark.parametrize("dtype,y8", [(BF, False), (BF, True), (F32, False)])
 @pytest.mark.parametrize("B,N,D", [(2, 4360, 3072), (1, 3001, 1024), (3, 1100, 2048), (1, 2500, 4104), (1, 2100, 8192),
-                                   (1, 20001, 256), (1, 60007, 32), (5, 1000, 520), (1, 1300, 16384), (1, 9001, 40)])
+                                   (1, 20001, 256), (1, 60007, 32), (5, 1000, 520), (1, 1300, 16384), (1, 9001, 40),
+                                   (3, 5001, 7), (1, 3000, 513), (2, 900, 1023), (1, 1200, 3001), (1, 40000, 13)])
 @pytest.mark.parametrize("post,pre,branch", [("none", "layer", True), ("layer", "rms", True), ("none", "rms", False)])
 def test_many_rows(af, B, N, D, dtype, y8, post, pre, branch):
     """Row counts at which a CTA takes several rounds of rows (more than twice

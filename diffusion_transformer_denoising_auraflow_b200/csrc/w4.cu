@@ -82,12 +82,12 @@ __device__ __forceinline__ void w4_values(const W4Raw& r, int f32, float (&v)[8]
 
 // ------------------------------------------------------------------ quantiser
 // Per row and group: a = max |w|, s = bf16(a / 7) to nearest even, c = 8 +
-// the whole number nearest to w / s (ties to even), 8 where s is zero.  The
-// division by 7 is an IEEE fp32 one, and so is w / s for fp32 weights: they
-// decide as real numbers would.  A border between two codes, (j + 1/2) s, and
-// one between two scales, times 7, are fp32 numbers (4 x 8 and 9 x 3 bits),
-// and a w or a next to one is off it by at least 2^-24 relative, which the
-// rounded quotient still shows.  bf16 weights are eight bits over eight bits:
+// the whole number nearest to w / s (ties to even), 8 where s is zero, decided
+// as real numbers would.  a / 7 is an IEEE fp32 division: a border between two
+// scales, times 7, is an fp32 number (9 x 3 bits), and an a next to one is off
+// it by at least 2^-24 relative, which the rounded quotient still shows.  For
+// fp32 weights a first guess w (1 / s) is put right by what it leaves, w - q s,
+// which fp32 holds exactly.  bf16 weights are eight bits over eight bits:
 // off a border (j + 1/2) by at least 2^-13, or on it, so w (1 / s) rounded to
 // a multiple of 2^-14 decides the same for a third of the instructions; and a
 // is never 7 times a border of s (an odd number of nine bits), so a (1 / 7) does.
@@ -121,16 +121,24 @@ __global__ void __launch_bounds__(256, F32 ? 4 : 6) quantize_rows_w4_kernel(cons
     for (int o = G / 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
     const uint16_t sb = static_cast<uint16_t>(pack_bf16(F32 ? __fdiv_rn(a, 7.0f) : a * (1.0f / 7.0f), 0.f));
     const float s = w4_bf16(sb);
-    // w / s rounded to a whole number, as a float; small scales (1 / s may
-    // overflow, few bits left) take the division
+    // w / s rounded to a whole number, as a float
     uint64_t c[4];  // columns 2 e and 2 e + 1
     if (F32 || s < 0x1p-100f) {
+      // the nearest of w (1 / s), put right by what is left of w: w - q s is exact
+      const float up = s < 0x1p-100f ? 0x1p100f : 1.0f, t = s * up, half = 0.5f * t;
+      const float inv = s > 0.f ? __fdividef(1.0f, t) : 0.f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         float d[2];
 #pragma unroll
-        for (int o = 0; o < 2; ++o)
-          d[o] = s > 0.f ? fminf(7.f, fmaxf(-8.f, rintf(__fdiv_rn(v[2 * e + o], s)))) : 0.f;
+        for (int o = 0; o < 2; ++o) {
+          const float x = v[2 * e + o] * up;
+          float n = rintf(x * inv);
+          const float left = fmaf(-n, t, x), mag = fabsf(left);
+          const bool odd = static_cast<int>(n) & 1;
+          if (mag > half || (mag == half && odd)) n += copysignf(1.0f, left);
+          d[o] = s > 0.f ? fminf(7.f, fmaxf(-8.f, n)) : 0.f;
+        }
         c[e] = w4_pack2(d[0], d[1]);
       }
     } else {
@@ -193,22 +201,44 @@ cudaError_t launch_quantize_rows_w4(const void* w, bool f32, int N, int K, int g
 // ------------------------------------------------------------------ values
 // The quantiser's tiles the other way round, bound by HBM too: a lane turns 4
 // bytes of codes into eight values.  8388608 + c is the pattern 0x4B000000 | c.
+template <bool VEC>
 __global__ void __launch_bounds__(256) dequantize_rows_w4_kernel(const uint8_t* __restrict__ codes,
                                                                  const uint16_t* __restrict__ scales,
                                                                  int scale_stride, int N, int K, int group,
-                                                                 void* __restrict__ out, int f32, int vec) {
+                                                                 void* __restrict__ out, int f32) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int chunks = (K + 255) / 256, tile = blockIdx.x / chunks;
   const int r0 = tile * 32 + warp * W4Q_ROWS, k = (blockIdx.x - tile * chunks) * 256 + lane * 8;
   const int groups = (K + group - 1) / group;
+  if constexpr (!VEC) {  // rows that are not whole vectors: a lane takes every 32nd column, so that stores are coalesced
+    const int k0 = k - lane * 8 + lane;
+#pragma unroll 1
+    for (int i = 0; i < W4Q_ROWS && r0 + i < N; ++i) {
+      const uint8_t* cr = codes + static_cast<size_t>(r0 + i) * groups * (group / 2);
+      uint8_t b[8];
+      uint16_t sb[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int kk = min(k0 + 32 * e, K - 1);
+        b[e] = cr[kk >> 1];
+        sb[e] = scales[static_cast<size_t>(kk / group) * scale_stride + r0 + i];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (k0 + 32 * e < K)
+          w4_store(out, f32, static_cast<size_t>(r0 + i) * K + k0 + 32 * e,
+                   w4_bf16(sb[e]) * (((b[e] >> (4 * (k0 & 1))) & 15) - 8));
+    }
+    return;
+  }
   if (k >= K) return;
   uint32_t w[W4Q_ROWS];
   float s[W4Q_ROWS];
 #pragma unroll
   for (int i = 0; i < W4Q_ROWS; ++i) {
-    if (r0 + i >= N) break;
-    w[i] = reinterpret_cast<const uint32_t*>(codes + static_cast<size_t>(r0 + i) * groups * (group / 2))[k >> 3];
-    s[i] = w4_bf16(scales[static_cast<size_t>(k / group) * scale_stride + r0 + i]);
+    const int n = min(r0 + i, N - 1);
+    w[i] = reinterpret_cast<const uint32_t*>(codes + static_cast<size_t>(n) * groups * (group / 2))[k >> 3];
+    s[i] = w4_bf16(scales[static_cast<size_t>(k / group) * scale_stride + n]);
   }
 #pragma unroll
   for (int i = 0; i < W4Q_ROWS; ++i) {
@@ -217,19 +247,13 @@ __global__ void __launch_bounds__(256) dequantize_rows_w4_kernel(const uint8_t* 
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       v[e] = s[i] * (__uint_as_float(((w[i] >> (4 * e)) & 15u) | 0x4B000000u) - 8388616.0f);
-    const size_t at = static_cast<size_t>(r0 + i) * K + k;
-    if (vec) {
-      uint4* d = reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) + at * (f32 ? 4 : 2));
-      if (f32) {
-        d[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-        d[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
-      } else {
-        d[0] = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-      }
+    uint4* d = reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) +
+                                        (static_cast<size_t>(r0 + i) * K + k) * (f32 ? 4 : 2));
+    if (f32) {
+      d[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+      d[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
     } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (k + e < K) w4_store(out, f32, at + e, v[e]);
+      d[0] = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
     }
   }
 }
@@ -238,8 +262,8 @@ cudaError_t launch_dequantize_rows_w4(const uint8_t* codes, const uint16_t* scal
                                       int group, void* out, bool f32, cudaStream_t s) {
   const int64_t grid = static_cast<int64_t>((K + 255) / 256) * ((N + 31) / 32);
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
-  dequantize_rows_w4_kernel<<<static_cast<unsigned>(grid), 256, 0, s>>>(codes, scales, scale_stride, N, K, group, out,
-                                                                       f32, w4_vec(out, K));
+  auto kernel = w4_vec(out, K) ? dequantize_rows_w4_kernel<true> : dequantize_rows_w4_kernel<false>;
+  kernel<<<static_cast<unsigned>(grid), 256, 0, s>>>(codes, scales, scale_stride, N, K, group, out, f32);
   return cudaGetLastError();
 }
 

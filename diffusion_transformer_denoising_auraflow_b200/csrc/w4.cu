@@ -24,7 +24,8 @@ __device__ __forceinline__ void w4_store(void* p, int f32, size_t i, float v) {
     static_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(pack_bf16(v, 0.f));
 }
 __device__ __forceinline__ float w4_bf16(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
-__device__ __forceinline__ float w4_silu(float a) { return a / (1.0f + expf(-a)); }
+// exp and division to a few last bits (2 + 1.2 |a| and 2): a third of the instructions of expf and a true division
+__device__ __forceinline__ float w4_silu(float a) { return __fdividef(a, 1.0f + __expf(-a)); }
 
 // packed fp32 pairs
 __device__ __forceinline__ uint64_t w4_pack2(float a, float b) {
@@ -296,11 +297,13 @@ cudaError_t launch_dequantize_rows_w4(const uint8_t* codes, const uint16_t* scal
 // dealt to g = 0..7 so that each load touches all 32 banks.  Of a word of
 // eight codes, p and p + 4 form one operand register; x lies in shared memory
 // in the order in which the lanes need it.
-constexpr int W4_WARPS = 16;
-constexpr int W4_THREADS = 32 * W4_WARPS;
-// Rows per warp by the 8-column blocks of x: 32 share the reads of x, with
-// more blocks than one 16 leave registers for four warps per scheduler.
-__host__ __device__ constexpr int w4_rows(int nt) { return nt == 1 ? 32 : 16; }
+// Warps of a CTA by the 8-column blocks of x: with more blocks than one the
+// registers of twelve (168 a thread) let 32 rows share the reads of x, and the
+// smaller rings leave shared memory for it.
+__host__ __device__ constexpr int w4_warps(int nt) { return nt == 1 ? 16 : 12; }
+constexpr int W4_ROWS = 32;                               // rows per warp
+// Rows of a warp whose sums are joined through shared memory at a time.
+__host__ __device__ constexpr int w4_red_rows(int nt) { return nt == 1 ? W4_ROWS : 16; }
 constexpr int W4_CHUNK = 256;                             // columns per chunk
 constexpr int W4_MAX_NT = 4;                              // 8-column blocks
 constexpr int W4_SMEM_MAX = 227 * 1024;
@@ -310,8 +313,8 @@ constexpr int W4_MAX_ROWS = W4_MAX_NT * 8 / 3;            // rows of x per CTA, 
 struct W4Launch {
   W4Params p;
   int rows_m;               // rows of x per CTA (blockIdx.y: which)
-  int rw;                   // row blocks per CTA tile; the other warps share a block's chunks
-  int tiles, chunks, seg_chunks, segs, stages;
+  int rw;                   // row blocks per CTA and round; W / rw warps share a block's chunks
+  int blocks, chunks, seg_chunks, segs, stages;
   int x_pitch;              // bytes between columns of x in shared memory
   int x_vec;                // x in 16-byte loads: aligned, K a multiple of 8
 };
@@ -370,24 +373,24 @@ struct W4X {
 // each digit one 8-byte store in the order 0, 2, 4, 6, 1, 3, 5, 7, as a word of
 // codes unpacks.  fac: what the chunk's sums of a digit stand for; off: minus
 // the magic number and 8 sum q of each group.  bad[m] is set if a value is not finite.
-template <int G, int NT>
+template <int G, int W, int NT>
 __device__ __forceinline__ void w4_stage_x(const W4Launch& L, int m0, int rows, const W4X& X, int* bad, int k0,
                                            int chunks) {
   const W4Params& p = L.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int U = 2;  // chunks per warp whose loads are in flight together
+  constexpr int U = NT == 1 ? 2 : 4;  // chunks per warp whose loads are in flight together
   const int items = rows * chunks;
-  for (int i0 = warp; i0 < items; i0 += U * W4_WARPS) {
+  for (int i0 = warp; i0 < items; i0 += U * W) {
     W4Raw raw[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int i = min(i0 + u * W4_WARPS, items - 1), m = i / chunks;
+      const int i = min(i0 + u * W, items - 1), m = i / chunks;
       raw[u] = w4_load8(p.x, p.x_f32, L.x_vec, static_cast<size_t>(m0 + m) * p.K,
                         k0 + 8 * ((i - m * chunks) * 32 + lane), p.K);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * W4_WARPS;
+      const int i = i0 + u * W;
       if (i >= items) break;
       const int m = i / chunks, c = i - m * chunks;
       float v[8], a = W4_TINY;
@@ -401,11 +404,11 @@ __device__ __forceinline__ void w4_stage_x(const W4Launch& L, int m0, int rows, 
       }
       asm volatile("redux.sync.max.abs.f32 %0, %0, 0xffffffff;" : "+f"(a));
       if (!fine) bad[m] = 1;
-      const float up = __fdiv_rn(W4_FIX, a);
+      const float up = __fdiv_rn(W4_FIX, a), down = __fdiv_rn(1.0f, up);
       uint32_t f[8];  // three signed bytes each: q = d0 + 256 d1 + 65536 d2
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        f[e] = (static_cast<uint32_t>(__float2int_rn(fminf(fmaxf(v[e] * up, -W4_FIX), W4_FIX))) + 0x808080u) ^ 0x808080u;
+        f[e] = (static_cast<uint32_t>(__float2int_rn(v[e] * up)) + 0x808080u) ^ 0x808080u;
 #pragma unroll
       for (int d = 0; d < 3; ++d) {
         const uint32_t sel = 0x40u + 0x11u * d;  // byte d of both
@@ -420,7 +423,7 @@ __device__ __forceinline__ void w4_stage_x(const W4Launch& L, int m0, int rows, 
                      : "memory");
         if (lane % (G / 8) == 0)
           sts_f1(X.off + ((c * (W4_CHUNK / G) + lane / (G / 8)) * (NT * 8) + col) * 4, -(W4_MAGIC + 8 * sum));
-        if (lane == d) sts_f1(X.fac + (c * (NT * 8) + col) * 4, __fdiv_rn(static_cast<float>(1 << (8 * d)), up));
+        if (lane == d) sts_f1(X.fac + (c * (NT * 8) + col) * 4, down * static_cast<float>(1 << (8 * d)));
       }
     }
   }
@@ -443,29 +446,30 @@ __device__ __forceinline__ void lds_words(uint32_t (&w)[N], uint32_t a) {
 }
 
 template <int NT, int G>
-__global__ void __launch_bounds__(W4_THREADS, 1)
+__global__ void __launch_bounds__(32 * w4_warps(NT), 1)
     linear_w4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_scales,
                      const __grid_constant__ W4Launch L) {
   extern __shared__ uint8_t w4_raw[];
-  constexpr int ROWS = w4_rows(NT), H = ROWS / 16;   // rows per warp, 16-row operands
+  constexpr int W = w4_warps(NT), THREADS = 32 * W;
+  constexpr int ROWS = W4_ROWS, H = ROWS / 16;       // rows per warp, 16-row operands
   constexpr int STAGE = ROWS * W4_CHUNK / 2;         // code bytes per stage
-  constexpr int RED_LD = ROWS + 4;                   // floats between columns of a warp's sums: few bank conflicts
-  __shared__ uint64_t full[W4_WARPS][W4_MAX_STAGES];
+  constexpr int RED = w4_red_rows(NT), RED_LD = RED + 4;  // rows of a warp joined at a time; floats between columns
+  __shared__ uint64_t full[W][W4_MAX_STAGES];
   __shared__ int abort_flag, bad[W4_MAX_ROWS];
   constexpr int GPC = W4_CHUNK / G;              // groups per chunk
   constexpr int WORDS = G / 32;                  // words of a lane per row and group
   constexpr int SC_STAGE = (ROWS * GPC * 2 + 127) / 128 * 128;  // scale bytes per stage
   const W4Params& p = L.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rw_n = L.rw, kw_n = W4_WARPS / rw_n;
+  const int rw_n = L.rw, kw_n = W / rw_n;
   const int rw = warp % rw_n, kw = warp / rw_n;
   const uint32_t base = (smem_u32(w4_raw) + 1023u) & ~1023u;
   const uint32_t codes_s = base + warp * L.stages * STAGE;
-  const uint32_t sc_s = base + W4_WARPS * L.stages * STAGE + warp * L.stages * SC_STAGE;
-  const uint32_t red_base = base + W4_WARPS * L.stages * (STAGE + SC_STAGE);
+  const uint32_t sc_s = base + W * L.stages * STAGE + warp * L.stages * SC_STAGE;
+  const uint32_t red_base = base + W * L.stages * (STAGE + SC_STAGE);
   const int m0 = blockIdx.y * L.rows_m, rows = min(L.rows_m, p.M - m0), cols = 3 * rows;
   W4X X;
-  X.x = red_base + W4_WARPS * NT * 8 * RED_LD * 4;
+  X.x = red_base + W * NT * 8 * RED_LD * 4;
   X.fac = X.x + 3 * L.rows_m * L.x_pitch;
   X.off = X.fac + L.seg_chunks * NT * 32;
   if (threadIdx.x < W4_MAX_ROWS) bad[threadIdx.x] = 0;
@@ -476,11 +480,14 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
   }
 
   const uint32_t bar0 = smem_u32(&full[warp][0]);
-  // this warp's stages in order: tile by tile, its chunks kw, kw + KW, ...
-  int ld_tile = kw < L.chunks ? blockIdx.x : L.tiles, ld_chunk = kw, ld_st = 0;  // the next to load (lane 0)
+  // this warp's stages in order: row block by row block, its chunks kw, kw + KW, ...
+  // Row blocks are dealt to the CTAs in turn, RW per round: in the last round
+  // every CTA has about as many as the others.
+  const int first_block = rw * gridDim.x + blockIdx.x, round_blocks = rw_n * gridDim.x;
+  int ld_block = kw < L.chunks ? first_block : L.blocks, ld_chunk = kw, ld_st = 0;  // the next to load (lane 0)
   auto load_next = [&] {
-    if (ld_tile >= L.tiles) return;
-    const int n0 = (ld_tile * rw_n + rw) * ROWS;
+    if (ld_block >= L.blocks) return;
+    const int n0 = ld_block * ROWS;
     const uint32_t bar = bar0 + 8 * ld_st;
     mbar_arrive_expect_tx(bar, STAGE + ROWS * GPC * 2);
     tma_load_2d(codes_s + ld_st * STAGE, &tm_codes, bar, ld_chunk * (W4_CHUNK / 2), n0);
@@ -489,7 +496,7 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
     ld_chunk += kw_n;
     if (ld_chunk >= L.chunks) {
       ld_chunk = kw;
-      ld_tile += gridDim.x;
+      ld_block += round_blocks;
     }
   };
   if (lane == 0) {
@@ -518,10 +525,11 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
   uint32_t ph = 0;
   if (L.segs == 1) {
     __syncthreads();  // bad[] is clear
-    w4_stage_x<G, NT>(L, m0, rows, X, bad, 0, L.seg_chunks);
+    w4_stage_x<G, W, NT>(L, m0, rows, X, bad, 0, L.seg_chunks);
     __syncthreads();  // (segs > 1: at the first part, before the first wait too)
   }
-  for (int tile = blockIdx.x; tile < L.tiles; tile += gridDim.x) {
+  for (int round = 0; round * round_blocks < L.blocks; ++round) {
+    const int block = first_block + round * round_blocks;
     uint64_t acc[H][NT][2];  // pairs of columns, rows r8 and r8 + 8
 #pragma unroll
     for (int h = 0; h < H; ++h)
@@ -531,11 +539,11 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
     for (int chunk = 0; chunk < L.chunks; chunk += kw_n, xc += kw_n) {
       if (L.segs > 1 && chunk % L.seg_chunks == 0) {  // x does not fit whole: its next part
         __syncthreads();
-        w4_stage_x<G, NT>(L, m0, rows, X, bad, chunk * W4_CHUNK, L.seg_chunks);
+        w4_stage_x<G, W, NT>(L, m0, rows, X, bad, chunk * W4_CHUNK, L.seg_chunks);
         __syncthreads();
         xc = kw;
       }
-      if (chunk + kw >= L.chunks) break;  // a last step that has no chunk for this warp
+      if (block >= L.blocks || chunk + kw >= L.chunks) continue;  // the last round, a last step: nothing for this warp
       if (ok) ok = mbar_wait(bar0 + 8 * st, ph, p.err, &abort_flag);
       if (ok) {
         const uint32_t row = codes_s + st * STAGE + mine;
@@ -606,40 +614,43 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
         ph ^= 1u;
       }
     }
-    // the tile's sums: a warp's rows by columns, then over the KW warps and the pieces of each row of x
-    if (kw_n > 1) __syncthreads();  // the last tile's are read
-    else __syncwarp();
+    // the round's sums, RED rows of each warp at a time: by columns, then over the KW warps and the pieces of a row of x
 #pragma unroll
-    for (int h = 0; h < H; ++h)
+    for (int h0 = 0; h0 < H; h0 += RED / 16) {
+      if (kw_n > 1) __syncthreads();  // the last ones are read
+      else __syncwarp();
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const uint32_t a = red + ((8 * i + 2 * t) * RED_LD + 16 * h + r8) * 4;
+      for (int h = 0; h < RED / 16; ++h)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          sts_f1(a + 32 * e, __uint_as_float(static_cast<uint32_t>(acc[h][i][e])));
-          sts_f1(a + 32 * e + RED_LD * 4, __uint_as_float(static_cast<uint32_t>(acc[h][i][e] >> 32)));
+        for (int i = 0; i < NT; ++i) {
+          const uint32_t a = red + ((8 * i + 2 * t) * RED_LD + 16 * h + r8) * 4;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            sts_f1(a + 32 * e, __uint_as_float(static_cast<uint32_t>(acc[h0 + h][i][e])));
+            sts_f1(a + 32 * e + RED_LD * 4, __uint_as_float(static_cast<uint32_t>(acc[h0 + h][i][e] >> 32)));
+          }
         }
+      if (kw_n > 1) __syncthreads();
+      else __syncwarp();
+      // all warps finish the rows of a KW > 1 round, else each its own
+      const int span = kw_n > 1 ? rw_n * RED : RED;
+      const int first = kw_n > 1 ? threadIdx.x : lane, step = kw_n > 1 ? THREADS : 32;
+      for (int i = first; i < span * rows; i += step) {
+        const int m = i / span, r = i - m * span, from = kw_n > 1 ? r / RED : rw;
+        const int n = ((round * rw_n + from) * gridDim.x + blockIdx.x) * ROWS + 16 * h0 + r % RED;
+        if (n >= p.N || !ok) continue;
+        float v = 0.f;
+        if (bad[m]) {
+          v = w4_plain_sum(p, m0 + m, n);
+        } else {
+          for (int d = 0; d < 3; ++d)
+            for (int k = 0; k < kw_n && k < L.chunks; ++k)
+              v += __uint_as_float(
+                  lds32(red_base + (((k * rw_n + from) * NT * 8 + 3 * m + d) * RED_LD + r % RED) * 4));
+        }
+        if (p.bias) v += p.bias[n];
+        w4_store(p.out, p.out_f32, static_cast<size_t>(m0 + m) * p.out_stride + n, v);
       }
-    if (kw_n > 1) __syncthreads();
-    else __syncwarp();
-    // all warps finish a KW > 1 tile's rows, else each its own
-    const int sh = __ffs(kw_n > 1 ? rw_n * ROWS : ROWS) - 1, span = 1 << sh;
-    const int first = kw_n > 1 ? threadIdx.x : lane, step = kw_n > 1 ? W4_THREADS : 32;
-    for (int i = first; i < span * rows; i += step) {
-      const int m = i >> sh, r = (i & (span - 1)) + (kw_n > 1 ? 0 : rw * ROWS);
-      const int n = tile * rw_n * ROWS + r;
-      if (n >= p.N || !ok) continue;
-      float v = 0.f;
-      if (bad[m]) {
-        v = w4_plain_sum(p, m0 + m, n);
-      } else {
-        for (int d = 0; d < 3; ++d)
-          for (int k = 0; k < kw_n && k < L.chunks; ++k)
-            v += __uint_as_float(lds32(red_base + (((k * rw_n + r / ROWS) * NT * 8 + 3 * m + d) * RED_LD +
-                                                   r % ROWS) * 4));
-      }
-      if (p.bias) v += p.bias[n];
-      w4_store(p.out, p.out_f32, static_cast<size_t>(m0 + m) * p.out_stride + n, v);
     }
   }
   if (!ok) {  // copies in flight land before the CTA ends
@@ -661,7 +672,7 @@ static cudaError_t linear_w4_launch(const W4Launch& L, const CUtensorMap& tc, co
     if (e != cudaSuccess) return e;
     done |= uint64_t(1) << dev;
   }
-  linear_w4_kernel<NT, G><<<grid, W4_THREADS, smem, s>>>(tc, ts, L);
+  linear_w4_kernel<NT, G><<<grid, 32 * w4_warps(NT), smem, s>>>(tc, ts, L);
   return cudaGetLastError();
 }
 
@@ -676,9 +687,9 @@ cudaError_t launch_linear_w4(const W4Params& p, cudaStream_t s) {
   L.x_vec = w4_vec(p.x, p.K);
   const int passes = (p.M + W4_MAX_ROWS - 1) / W4_MAX_ROWS;
   L.rows_m = (p.M + passes - 1) / passes;
-  const int cols = 3 * L.rows_m, nt = (cols + 7) / 8, rows = w4_rows(nt);
-  const int stage = W4_WARPS * (rows * W4_CHUNK / 2 + (rows * (W4_CHUNK / p.group) * 2 + 127) / 128 * 128);
-  const int fixed = W4_WARPS * nt * 8 * (rows + 4) * 4 + 3072;  // sums, alignment, static barriers
+  const int cols = 3 * L.rows_m, nt = (cols + 7) / 8, warps = w4_warps(nt), rows = W4_ROWS;
+  const int stage = warps * (rows * W4_CHUNK / 2 + rows * (W4_CHUNK / p.group) * 2);
+  const int fixed = warps * nt * 8 * (w4_red_rows(nt) + 4) * 4 + 3072;  // sums, alignment, static barriers
   // x lies in shared memory whole if two stages fit beside it, else in parts
   // of `seg` chunks, a multiple of the chunks that share a row; columns are
   // spaced so that the lanes of a bank cycle differ
@@ -687,23 +698,24 @@ cudaError_t launch_linear_w4(const W4Params& p, cudaStream_t s) {
   const int room = (W4_SMEM_MAX - fixed - 2 * stage - cols * pad) / chunk_bytes;  // chunks
   const bool whole = L.chunks <= room;
   const int per = passes < sms ? sms / passes : 1;  // CTAs per part of x's rows
-  // the split with the least time on the busiest SM: rounds of tiles, each a
-  // chunk time per stage, the tile's bytes and a fixed end
+  // the split with the least time on the busiest SM: rounds of row blocks, each
+  // a chunk time per step, the round's bytes and a fixed end
+  L.blocks = (p.N + rows - 1) / rows;
   float best = 0.f;
   L.rw = 0;
-  for (int rw = W4_WARPS; rw >= 1; rw /= 2) {
-    const int tiles = (p.N + rw * rows - 1) / (rw * rows), kw = W4_WARPS / rw;
+  for (int rw = warps; rw >= 1; --rw) {
+    if (warps % rw) continue;
+    const int kw = warps / rw;
     if (!whole && kw > room) break;
-    const float cost = static_cast<float>((tiles + per - 1) / per) *
-                       (0.5f * ((L.chunks + kw - 1) / kw) + 0.5f * rw * L.chunks / W4_WARPS + 0.5f);
+    const float cost = static_cast<float>((L.blocks + rw * per - 1) / (rw * per)) *
+                       (0.5f * ((L.chunks + kw - 1) / kw) + 0.5f * rw * L.chunks / warps + 0.5f);
     if (L.rw == 0 || cost < best) {
       best = cost;
       L.rw = rw;
-      L.tiles = tiles;
     }
   }
   if (L.rw == 0 || passes > 65535) return cudaErrorInvalidValue;
-  const int kw = W4_WARPS / L.rw;
+  const int kw = warps / L.rw;
   L.seg_chunks = whole ? L.chunks : room / kw * kw;
   L.segs = (L.chunks + L.seg_chunks - 1) / L.seg_chunks;
   L.x_pitch = L.seg_chunks * W4_CHUNK + pad;
@@ -716,7 +728,8 @@ cudaError_t launch_linear_w4(const W4Params& p, cudaStream_t s) {
       !encode_tmap_2d(&ts, p.scales, p.N, groups, static_cast<uint64_t>(p.scale_stride) * 2, rows,
                       W4_CHUNK / p.group, false, 0))
     return cudaErrorInvalidValue;
-  const dim3 grid(L.tiles < per ? L.tiles : per, passes);
+  const int need = (L.blocks + L.rw - 1) / L.rw;
+  const dim3 grid(need < per ? need : per, passes);
 #define AF_W4_CASE(NT_)                                                            \
   if (nt == NT_)                                                                   \
     return p.group == 32   ? linear_w4_launch<NT_, 32>(L, tc, ts, smem, grid, s)   \

@@ -7,9 +7,10 @@ most d u sum |t_i|, with u = 2^-23 (a tensor-core addition may truncate
 instead of rounding to half a step).  A chain passes at most K / 16 steps of
 16 columns, K / 32 groups, 32 partial sums and a few last additions:
 d = K / 16 + K / 32 + 48.  x enters as 24-bit fixed point, off by at most half
-an fp32 step (2^-24) of the largest magnitude among its 256 columns.  SiLU adds
-the errors of exp, the sum and the division, held to 8 u of a term.  bf16
-output adds half a step, 2^-8 relative.
+an fp32 step (2^-24) of the largest magnitude among its 256 columns.  SiLU of
+|x| <= 5 adds the errors of exp (2 + 1.2 |x| steps), the sum (1/2) and the
+division (2): at most 11 u of a term.  bf16 output adds half a step, 2^-8
+relative.
 """
 import numpy as np
 import pytest
@@ -52,7 +53,7 @@ def _scales(s, n):
 def _tol(x, w, K, silu, out_dtype, ref):
     ax = np.abs(x)
     top = np.pad(ax, ((0, 0), (0, -K % 256))).reshape(len(x), -1, 256).max(-1).repeat(256, 1)[:, :K]
-    t = ((K / 16 + K / 32 + 48 + (8 if silu else 0)) * U * ax + 2.0 ** -24 * top) @ np.abs(w).T + 1e-30
+    t = ((K / 16 + K / 32 + 48 + (11 if silu else 0)) * U * ax + 2.0 ** -24 * top) @ np.abs(w).T + 1e-30
     return t + (np.abs(ref) * 2.0 ** -8 if out_dtype == BF else np.abs(ref) * U)
 
 

@@ -632,24 +632,30 @@ __global__ void __launch_bounds__(32 * w4_warps(NT), 1)
         }
       if (kw_n > 1) __syncthreads();
       else __syncwarp();
-      // all warps finish the rows of a KW > 1 round, else each its own
-      const int span = kw_n > 1 ? rw_n * RED : RED;
-      const int first = kw_n > 1 ? threadIdx.x : lane, step = kw_n > 1 ? THREADS : 32;
-      for (int i = first; i < span * rows; i += step) {
-        const int m = i / span, r = i - m * span, from = kw_n > 1 ? r / RED : rw;
-        const int n = ((round * rw_n + from) * gridDim.x + blockIdx.x) * ROWS + 16 * h0 + r % RED;
-        if (n >= p.N || !ok) continue;
+      auto finish = [&](int m, int from, int r) {  // row r of the block of the row warps' `from`
+        const int n = ((round * rw_n + from) * gridDim.x + blockIdx.x) * ROWS + 16 * h0 + r;
+        if (n >= p.N || !ok) return;
         float v = 0.f;
         if (bad[m]) {
           v = w4_plain_sum(p, m0 + m, n);
         } else {
-          for (int d = 0; d < 3; ++d)
-            for (int k = 0; k < kw_n && k < L.chunks; ++k)
-              v += __uint_as_float(
-                  lds32(red_base + (((k * rw_n + from) * NT * 8 + 3 * m + d) * RED_LD + r % RED) * 4));
+          const uint32_t at = red_base + ((from * NT * 8 + 3 * m) * RED_LD + r) * 4;
+          for (int k = 0; k < kw_n && k < L.chunks; ++k)
+#pragma unroll
+            for (int d = 0; d < 3; ++d)
+              v += __uint_as_float(lds32(at + (k * rw_n * NT * 8 + d) * RED_LD * 4));
         }
         if (p.bias) v += p.bias[n];
         w4_store(p.out, p.out_f32, static_cast<size_t>(m0 + m) * p.out_stride + n, v);
+      };
+      // all warps finish the rows of a KW > 1 round, else each its own
+      if (kw_n > 1) {
+        for (int i = threadIdx.x; i < rw_n * RED * rows; i += THREADS) {
+          const int q = i / RED, m = q / rw_n;
+          finish(m, q - m * rw_n, i % RED);
+        }
+      } else {
+        for (int i = lane; i < RED * rows; i += 32) finish(i / RED, rw, i % RED);
       }
     }
   }

@@ -378,53 +378,51 @@ __device__ __forceinline__ void w4_stage_x(const W4Launch& L, int m0, int rows, 
                                            int chunks) {
   const W4Params& p = L.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int U = NT == 1 ? 2 : 4;  // chunks per warp whose loads are in flight together
   const int items = rows * chunks;
-  for (int i0 = warp; i0 < items; i0 += U * W) {
-    W4Raw raw[U];
+  auto load = [&](int i) {
+    const int j = min(i, items - 1), m = j / chunks;
+    return w4_load8(p.x, p.x_f32, L.x_vec, static_cast<size_t>(m0 + m) * p.K, k0 + 8 * ((j - m * chunks) * 32 + lane),
+                    p.K);
+  };
+  // the next item's loads are in flight while one is converted; one body, as
+  // its instructions are fetched anew by every small call
+  W4Raw next = load(warp);
+#pragma unroll 1
+  for (int i = warp; i < items; i += W) {
+    const W4Raw raw = next;
+    next = load(i + W);
+    const int m = i / chunks, c = i - m * chunks;
+    float v[8], a = W4_TINY;
+    w4_values(raw, p.x_f32, v);
+    bool fine = true;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = min(i0 + u * W, items - 1), m = i / chunks;
-      raw[u] = w4_load8(p.x, p.x_f32, L.x_vec, static_cast<size_t>(m0 + m) * p.K,
-                        k0 + 8 * ((i - m * chunks) * 32 + lane), p.K);
+    for (int e = 0; e < 8; ++e) {
+      if (p.silu) v[e] = w4_silu(v[e]);
+      a = fmaxf(a, fabsf(v[e]));
+      fine &= fabsf(v[e]) < INFINITY;
     }
+    asm volatile("redux.sync.max.abs.f32 %0, %0, 0xffffffff;" : "+f"(a));
+    if (!fine) bad[m] = 1;
+    const float up = __fdiv_rn(W4_FIX, a), down = __fdiv_rn(1.0f, up);
+    uint32_t f[8];  // three signed bytes each: q = d0 + 256 d1 + 65536 d2
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * W;
-      if (i >= items) break;
-      const int m = i / chunks, c = i - m * chunks;
-      float v[8], a = W4_TINY;
-      w4_values(raw[u], p.x_f32, v);
-      bool fine = true;
+    for (int e = 0; e < 8; ++e)
+      f[e] = (static_cast<uint32_t>(__float2int_rn(v[e] * up)) + 0x808080u) ^ 0x808080u;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (p.silu) v[e] = w4_silu(v[e]);
-        a = fmaxf(a, fabsf(v[e]));
-        fine &= fabsf(v[e]) < INFINITY;
-      }
-      asm volatile("redux.sync.max.abs.f32 %0, %0, 0xffffffff;" : "+f"(a));
-      if (!fine) bad[m] = 1;
-      const float up = __fdiv_rn(W4_FIX, a), down = __fdiv_rn(1.0f, up);
-      uint32_t f[8];  // three signed bytes each: q = d0 + 256 d1 + 65536 d2
+    for (int d = 0; d < 3; ++d) {
+      const uint32_t sel = 0x40u + 0x11u * d;  // byte d of both
+      const uint32_t lo = __byte_perm(__byte_perm(f[0], f[2], sel), __byte_perm(f[4], f[6], sel), 0x5410);
+      const uint32_t hi = __byte_perm(__byte_perm(f[1], f[3], sel), __byte_perm(f[5], f[7], sel), 0x5410);
+      int sum = __dp4a(static_cast<int>(lo), 0x01010101, __dp4a(static_cast<int>(hi), 0x01010101, 0));
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        f[e] = (static_cast<uint32_t>(__float2int_rn(v[e] * up)) + 0x808080u) ^ 0x808080u;
-#pragma unroll
-      for (int d = 0; d < 3; ++d) {
-        const uint32_t sel = 0x40u + 0x11u * d;  // byte d of both
-        const uint32_t lo = __byte_perm(__byte_perm(f[0], f[2], sel), __byte_perm(f[4], f[6], sel), 0x5410);
-        const uint32_t hi = __byte_perm(__byte_perm(f[1], f[3], sel), __byte_perm(f[5], f[7], sel), 0x5410);
-        int sum = __dp4a(static_cast<int>(lo), 0x01010101, __dp4a(static_cast<int>(hi), 0x01010101, 0));
-#pragma unroll
-        for (int o = G / 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const int col = 3 * m + d;
-        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(X.x + col * L.x_pitch + 8 * (c * 32 + lane)), "r"(lo),
-                     "r"(hi)
-                     : "memory");
-        if (lane % (G / 8) == 0)
-          sts_f1(X.off + ((c * (W4_CHUNK / G) + lane / (G / 8)) * (NT * 8) + col) * 4, -(W4_MAGIC + 8 * sum));
-        if (lane == d) sts_f1(X.fac + (c * (NT * 8) + col) * 4, down * static_cast<float>(1 << (8 * d)));
-      }
+      for (int o = G / 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      const int col = 3 * m + d;
+      asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(X.x + col * L.x_pitch + 8 * (c * 32 + lane)), "r"(lo),
+                   "r"(hi)
+                   : "memory");
+      if (lane % (G / 8) == 0)
+        sts_f1(X.off + ((c * (W4_CHUNK / G) + lane / (G / 8)) * (NT * 8) + col) * 4, -(W4_MAGIC + 8 * sum));
+      if (lane == d) sts_f1(X.fac + (c * (NT * 8) + col) * 4, down * static_cast<float>(1 << (8 * d)));
     }
   }
 }

@@ -202,6 +202,24 @@ __device__ __forceinline__ RnRaw<T> rn_load8(const void* p, size_t i) {
   for (int e = 0; e < static_cast<int>(sizeof(T) / 2); ++e) r.q[e] = s[e];
   return r;
 }
+// The same for the columns before `end`, zero behind it.
+template <typename T>
+__device__ __forceinline__ RnRaw<T> rn_load_some(const void* p, int64_t i, int64_t end) {
+  uint32_t w[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if constexpr (sizeof(T) == 4) w[e] = i + e < end ? static_cast<const uint32_t*>(p)[i + e] : 0u;
+    else w[e] = i + e < end ? static_cast<const uint16_t*>(p)[i + e] : 0u;
+  }
+  RnRaw<T> r;
+  if constexpr (sizeof(T) == 4) {
+    r.q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    r.q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  } else {
+    r.q[0] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+  }
+  return r;
+}
 template <typename T>
 __device__ __forceinline__ void rn_expand(const RnRaw<T>& r, uint64_t (&v)[4]) {
   if constexpr (sizeof(T) == 4) {
@@ -239,6 +257,9 @@ struct RnPlan {
   int staged;      // factors in shared memory
   int stages;      // RING: rows in flight per row group
 };
+// Floats of a plane of the shifted kernel's factors: an entry before and one
+// behind the columns, and 4 mod 32 so that eight planes fill the banks.
+__host__ __device__ constexpr int rn_plane(int D) { return ((D + 7) / 8 + 2 + 27) / 32 * 32 + 4; }
 constexpr int RN_SMEM_MAX = 222 * 1024;  // beside the static barriers and sums
 constexpr int RN_RING_THREADS = 672;  // 21 warps of 80 registers
 constexpr int RN_MAX_GROUPS = 21, RN_MAX_STAGES = 8;
@@ -517,6 +538,211 @@ __global__ void __launch_bounds__(RING ? RN_RING_THREADS : 512, V == 1 ? 2 : 1)
   }
 }
 
+// ------------------------------------------------------------------ many rows of any width
+// Widths that are not multiples of 8: a row starts anywhere in a 16-byte
+// vector, so threads hold the aligned vectors that the row touches.  Element e
+// of vector g is column 8 g + e - off, off = the row's first element mod 8; in
+// the first and the last vector some of the eight belong to the neighbouring
+// rows: they are read with the rest, taken as zero, and not written.  Factors
+// lie in shared memory in eight planes by column mod 8, where the lanes' columns
+// 8 apart are neighbours whatever off is.
+template <typename T, bool OUT8, int V>
+__global__ void __launch_bounds__(512, 1)
+    residual_norm_shift_kernel(const __grid_constant__ ResidualNormParams p, const RnPlan plan) {
+  extern __shared__ __align__(16) float factors[];  // [3][8][plane]
+  __shared__ float red[15][2][16];
+  const int tg = plan.tg, warps = tg >> 5, D = p.D;
+  const int plane = rn_plane(D);
+  const int grp = threadIdx.x / tg, tid = threadIdx.x - grp * tg;
+  const int lane = threadIdx.x & 31, warp = tid >> 5;
+  const int b = blockIdx.x / plan.per, cta = blockIdx.x - b * plan.per;
+  const int g0 = warps ? warp * (32 * V) + lane : tid;  // this thread's vectors: g0 + 32 i
+  const int64_t sample = static_cast<int64_t>(b) * p.rows_per_batch;
+  const int64_t total = static_cast<int64_t>(p.B) * p.rows_per_batch * D;
+  const size_t mo = static_cast<size_t>(b) * p.mod_stride;
+  for (int d = threadIdx.x; d < D; d += blockDim.x) {
+    float f = p.residual_scale, m = 1.f;
+    if (p.gate) f *= __ldg(p.gate + mo + d);
+    if (p.post_weight) f *= __ldg(p.post_weight + d);
+    if (p.scale) m += __ldg(p.scale + mo + d);
+    if (p.pre_weight) m *= __ldg(p.pre_weight + d);
+    float* at = factors + (d & 7) * plane + (d >> 3) + 1;
+    at[0] = f;
+    at[8 * plane] = m;
+    at[16 * plane] = p.shift ? __ldg(p.shift + mo + d) : 0.f;
+  }
+  __syncthreads();
+  int buf = 0;
+  auto join = [&](float s, bool max) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      if (warps == 0 && o >= tg) continue;
+      const float t = __shfl_xor_sync(0xffffffffu, s, o);
+      s = max ? fmaxf(s, t) : s + t;
+    }
+    if (warps <= 1) return s;
+    float* r = red[grp][buf];
+    buf ^= 1;
+    if (lane == 0) r[warp] = s;
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "r"(tg) : "memory");
+    s = r[0];
+    for (int i = 1; i < warps; ++i) s = max ? fmaxf(s, r[i]) : s + r[i];
+    return s;
+  };
+  auto off_of = [&](int r) { return static_cast<int>((((sample + r) & 7) * (D & 7)) & 7); };
+  RnRaw<T> xq[V], bq[V];
+  auto fetch = [&](int r) {
+    if (r >= p.rows_per_batch) return;
+    const int off = off_of(r);
+    const int64_t first = (sample + r) * D - off;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int g = g0 + 32 * i;
+      const int64_t at = first + 8 * g;
+      xq[i] = RnRaw<T>{};
+      bq[i] = RnRaw<T>{};
+      if (8 * g >= off + D) continue;
+      if (at + 8 <= total) {
+        xq[i] = rn_load8<T>(p.x, at);
+        if (p.branch) bq[i] = rn_load8<T>(p.branch, at);
+      } else {  // the tensors end inside the vector
+        xq[i] = rn_load_some<T>(p.x, at, total);
+        if (p.branch) bq[i] = rn_load_some<T>(p.branch, at, total);
+      }
+    }
+  };
+  const float inv_d = 1.0f / static_cast<float>(D);
+  const int step = plan.per * plan.groups;
+  int r = cta + plan.per * grp;
+  const int ahead = warps ? 0 : lane / tg * plan.per;
+  fetch(r);
+  for (; r - ahead < p.rows_per_batch; r += step) {
+    const bool live = r < p.rows_per_batch;
+    const int off = live ? off_of(r) : 0;
+    const int64_t first = (sample + r) * D - off;
+    uint32_t mask[V];  // which of the eight are the row's
+    float x[V][8], u[V][8];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int g = g0 + 32 * i, end = off + D - 8 * g;
+      mask[i] = !live || end <= 0 ? 0u : (0xFFu << (g == 0 ? off : 0)) & (end >= 8 ? 0xFFu : (1u << end) - 1u);
+      uint64_t v[4];
+      auto put = [&](const RnRaw<T>& q, float (&o)[8]) {
+        rn_expand<T>(q, v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = rn_unpack(v[e]);
+          o[2 * e] = f.x;
+          o[2 * e + 1] = f.y;
+        }
+        if (mask[i] != 0xFFu) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (!((mask[i] >> e) & 1u)) o[e] = 0.f;
+        }
+      };
+      put(xq[i], x[i]);
+      put(bq[i], u[i]);
+    }
+    fetch(r + step);
+    // element e's factor: column 8 g + e - off
+    auto factor = [&](int which, int g, int e) {
+      const int c = e - off;
+      return factors[(8 * which + (c & 7)) * plane + g + (c >> 3) + 1];
+    };
+    auto normalise = [&](float (&v)[V][8], int kind) {
+      if (kind == NORM_NONE) return;
+      float mean = 0.f, q = 0.f;
+      if (kind == NORM_LAYER) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) mean += v[i][e];
+        mean = join(mean, false) * inv_d;
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[i][e] -= mean;
+        if (mask[i] != 0xFFu) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (!((mask[i] >> e) & 1u)) v[i][e] = 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q = fmaf(v[i][e], v[i][e], q);
+      }
+      const float f = rsqrtf(join(q, false) * inv_d + p.eps);
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[i][e] *= f;
+    };
+    auto store = [&](void* t, int i, const float (&v)[8]) {
+      const int64_t at = first + 8 * (g0 + 32 * i);
+      if (mask[i] == 0xFFu) {
+        const uint64_t o[4] = {rn_pack(v[0], v[1]), rn_pack(v[2], v[3]), rn_pack(v[4], v[5]), rn_pack(v[6], v[7])};
+        rn_store8<T>(t, at, o);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if ((mask[i] >> e) & 1u) rn_store<T>(t, at + e, v[e]);
+      }
+    };
+    if (p.branch) {
+      normalise(u, p.post);
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (mask[i]) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[i][e] = fmaf(factor(0, g0 + 32 * i, e), u[i][e], x[i][e]);
+          if (mask[i] != 0xFFu) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (!((mask[i] >> e) & 1u)) x[i][e] = 0.f;
+          }
+        }
+    }
+    if (p.x_out) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (mask[i]) store(p.x_out, i, x[i]);
+    }
+    if (!p.y) continue;
+    normalise(x, p.pre);
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (!mask[i]) continue;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[i][e] = fmaf(x[i][e], factor(1, g0 + 32 * i, e), factor(2, g0 + 32 * i, e));
+        if (OUT8 && ((mask[i] >> e) & 1u)) amax = fmaxf(amax, fabsf(x[i][e]));
+      }
+      if constexpr (!OUT8) store(p.y, i, x[i]);
+    }
+    if constexpr (OUT8) {
+      amax = join(amax, true);
+      const float inv = amax > 0.f ? 448.0f / amax : 1.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (!mask[i]) continue;
+        const uint32_t lo = pack_e4m3x4(x[i][0] * inv, x[i][1] * inv, x[i][2] * inv, x[i][3] * inv);
+        const uint32_t hi = pack_e4m3x4(x[i][4] * inv, x[i][5] * inv, x[i][6] * inv, x[i][7] * inv);
+        uint8_t* at = static_cast<uint8_t*>(p.y) + first + 8 * (g0 + 32 * i);
+        if (mask[i] == 0xFFu) {
+          *reinterpret_cast<uint2*>(at) = make_uint2(lo, hi);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if ((mask[i] >> e) & 1u) at[e] = static_cast<uint8_t>((e < 4 ? lo : hi) >> (8 * (e & 3)));
+        }
+      }
+      if (tid == 0 && live) p.yscale[sample + r] = amax > 0.f ? amax / 448.0f : 1.0f;
+    }
+  }
+}
+
 }  // namespace
 
 template <typename T, bool OUT8, int V, bool EXACT, bool RING>
@@ -564,7 +790,7 @@ static cudaError_t rn_launch(const ResidualNormParams& p, cudaStream_t s) {
     if (plan.groups > p.rows_per_batch && plan.tg >= 32) plan.groups = p.rows_per_batch;
     return (p.rows_per_batch + plan.groups - 1) / plan.groups;  // rounds of a sample's rows
   };
-  const int one = (sms + p.B - 1) / p.B;  // CTAs per sample at one per SM
+  const int one = max(1, sms / p.B);  // CTAs per sample at one per SM
   plan.stages = 0;
   int rounds = split(RN_RING_THREADS);
   if (v > 1 && rounds > 2 * one) {
@@ -574,7 +800,7 @@ static cudaError_t rn_launch(const ResidualNormParams& p, cudaStream_t s) {
   const bool ring = plan.stages > 0;
   if (!ring) rounds = split(512);
   const int threads = plan.tg * plan.groups;
-  const int want = ring ? one : ((v == 1 ? 1024 : 512) / threads * sms + p.B - 1) / p.B;
+  const int want = ring ? one : max(1, (v == 1 ? 1024 : 512) / threads * sms / p.B);
   plan.per = rounds < want ? rounds : want;
   plan.staged = rounds > plan.per;
   const unsigned grid = static_cast<unsigned>(p.B) * plan.per;
@@ -596,9 +822,46 @@ static cudaError_t rn_launch(const ResidualNormParams& p, cudaStream_t s) {
   return cudaErrorInvalidValue;
 }
 
+template <typename T, bool OUT8, int V>
+static cudaError_t rn_shift(const ResidualNormParams& p, const RnPlan& plan, cudaStream_t s) {
+  static uint64_t done = 0;  // one bit per device: the kernel's shared-memory opt-in
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (!((done >> dev) & 1u)) {
+    const cudaError_t e = cudaFuncSetAttribute(residual_norm_shift_kernel<T, OUT8, V>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, RN_SMEM_MAX);
+    if (e != cudaSuccess) return e;
+    done |= uint64_t(1) << dev;
+  }
+  residual_norm_shift_kernel<T, OUT8, V><<<static_cast<unsigned>(p.B) * plan.per, plan.tg * plan.groups,
+                                           24 * rn_plane(p.D) * sizeof(float), s>>>(p, plan);
+  return cudaGetLastError();
+}
+
 template <typename T, bool OUT8>
-static cudaError_t rn_any(const ResidualNormParams& p, cudaStream_t s) {
+static cudaError_t rn_any(const ResidualNormParams& p, bool aligned, cudaStream_t s) {
   const size_t rows = static_cast<size_t>(p.B) * p.rows_per_batch;
+  static int sms = 0;
+  if (!sms) sms = device_sm_count();
+  // enough rows for every SM to take several: aligned vectors of each row
+  const int nv = (p.D + 14) / 8;  // vectors that a row may touch
+  RnPlan plan{};
+  plan.tg = 4;
+  while (plan.tg < 32 && plan.tg < nv) plan.tg *= 2;
+  if (nv > 32) plan.tg = (nv + 127) / 128 * 32;
+  if (aligned && plan.tg <= 512) {
+    const int v = plan.tg < 32 ? 1 : (nv + plan.tg - 1) / plan.tg;
+    plan.groups = 512 / plan.tg;
+    if (plan.tg > 32 && plan.groups > 15) plan.groups = 15;
+    const int one = max(1, sms / p.B), rounds = (p.rows_per_batch + plan.groups - 1) / plan.groups;
+    plan.per = rounds < one ? rounds : one;
+    if (rounds >= 2 * one) {
+      if (v == 1) return rn_shift<T, OUT8, 1>(p, plan, s);
+      if (v == 2) return rn_shift<T, OUT8, 2>(p, plan, s);
+      if (v == 3) return rn_shift<T, OUT8, 3>(p, plan, s);
+      return rn_shift<T, OUT8, 4>(p, plan, s);
+    }
+  }
   int tg = 4, threads = RN_THREADS;
   if (p.D <= 128) {  // four columns a thread
     while (tg < 32 && tg * 4 < p.D) tg *= 2;
@@ -618,13 +881,13 @@ static cudaError_t rn_any(const ResidualNormParams& p, cudaStream_t s) {
 
 cudaError_t launch_residual_norm(const ResidualNormParams& p, bool f32, cudaStream_t s) {
   auto al = [](const void* a) { return (reinterpret_cast<uintptr_t>(a) & 15) == 0; };
-  const bool vec = p.D % 8 == 0 && al(p.x) && al(p.branch) && al(p.x_out) && al(p.y);
+  const bool aligned = al(p.x) && al(p.branch) && al(p.x_out) && al(p.y), vec = aligned && p.D % 8 == 0;
   if (p.yscale) {
     if (vec) return f32 ? rn_launch<float, true>(p, s) : rn_launch<uint16_t, true>(p, s);
-    return f32 ? rn_any<float, true>(p, s) : rn_any<uint16_t, true>(p, s);
+    return f32 ? rn_any<float, true>(p, aligned, s) : rn_any<uint16_t, true>(p, aligned, s);
   }
   if (vec) return f32 ? rn_launch<float, false>(p, s) : rn_launch<uint16_t, false>(p, s);
-  return f32 ? rn_any<float, false>(p, s) : rn_any<uint16_t, false>(p, s);
+  return f32 ? rn_any<float, false>(p, aligned, s) : rn_any<uint16_t, false>(p, aligned, s);
 }
 
 }  // namespace af

@@ -120,7 +120,8 @@ def test_matches_oracle(af, B, N, D, dtype, post, pre, gate, mod, pw, qw, r):
 @pytest.mark.parametrize("dtype,y8", [(BF, False), (BF, True), (F32, False)])
 @pytest.mark.parametrize("B,N,D", [(2, 4360, 3072), (1, 3001, 1024), (3, 1100, 2048), (1, 2500, 4104), (1, 2100, 8192),
                                    (1, 20001, 256), (1, 60007, 32), (5, 1000, 520), (1, 1300, 16384), (1, 9001, 40),
-                                   (3, 5001, 7), (1, 3000, 513), (2, 900, 1023), (1, 1200, 3001), (1, 40000, 13)])
+                                   (3, 5001, 7), (1, 3000, 513), (2, 900, 1023), (1, 1200, 3001), (1, 40000, 13),
+                                   (2, 7000, 101), (1, 70001, 1), (1, 5000, 250), (1, 2400, 3999), (1, 700, 16001)])
 @pytest.mark.parametrize("post,pre,branch", [("none", "layer", True), ("layer", "rms", True), ("none", "rms", False)])
 def test_many_rows(af, B, N, D, dtype, y8, post, pre, branch):
     """Row counts at which a CTA takes several rounds of rows (more than twice
@@ -200,6 +201,26 @@ def test_in_place(af, D, dtype):
     assert torch.equal(xi, xo) and torch.equal(bi, y)
     xi = xd.clone()
     af.residual_norm(xi, bd, None, xi, EPS, **kw)
+    assert torch.equal(xi, y)
+
+
+@pytest.mark.parametrize("N,D,dtype", [(4400, 3072, BF), (6000, 1001, BF), (5000, 1014, F32), (30000, 45, BF),
+                                       (9000, 1024, BF)])
+def test_in_place_many_rows(af, N, D, dtype):
+    """Rows are read ahead of the ones being written, and odd widths share
+    vectors with their neighbours: in place must not change a bit."""
+    g = torch.Generator(device="cuda").manual_seed(922)
+    x = torch.randn(2, N, D, device="cuda", generator=g).to(dtype)
+    b = torch.randn(2, N, D, device="cuda", generator=g).to(dtype)
+    t = torch.randn(2, 3 * D, device="cuda", generator=g)
+    kw = dict(gate=t, shift=t[:, D:], scale=t[:, 2 * D:], mod_stride=3 * D, post="rms", pre="layer")
+    xo, y = torch.empty_like(x), torch.empty_like(x)
+    af.residual_norm(x, b, xo, y, EPS, **kw)
+    xi, bi = x.clone(), b.clone()
+    af.residual_norm(xi, bi, xi, bi, EPS, **kw)
+    assert torch.equal(xi, xo) and torch.equal(bi, y)
+    xi = x.clone()
+    af.residual_norm(xi, b, None, xi, EPS, **kw)
     assert torch.equal(xi, y)
 
 

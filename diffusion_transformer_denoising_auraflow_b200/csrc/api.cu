@@ -1798,6 +1798,7 @@ af_status af_linear_w4(const void* x, int x_dtype, int silu, const uint8_t* code
                        void* stream) {
   if (!x || !out || M <= 0 || !is_dtype(x_dtype) || !is_dtype(out_dtype)) return AF_ERR_INVALID_ARG;
   AF_TRY(check_w4(codes, scales, scale_stride, N, K, group));
+  if (M > LINEAR_W4_MAX_M) return AF_ERR_UNSUPPORTED;
   const W4Params p{x, codes, scales, bias, out, M, N, K, group, scale_stride, N, x_dtype == AF_DTYPE_F32,
                    out_dtype == AF_DTYPE_F32, silu != 0};
   AF_CUDA(launch_linear_w4(p, static_cast<cudaStream_t>(stream)));
@@ -1810,7 +1811,7 @@ static af_status residual_norm_call(ResidualNormParams p, int dtype, int N, void
   if (p.post < NORM_NONE || p.post > NORM_RMS || p.pre < NORM_NONE || p.pre > NORM_RMS) return AF_ERR_INVALID_ARG;
   if (!p.branch && (p.gate || p.post_weight || p.post != NORM_NONE)) return AF_ERR_INVALID_ARG;
   if (!p.y && (p.shift || p.scale || p.pre_weight)) return AF_ERR_INVALID_ARG;
-  if (p.D > 16384 || static_cast<int64_t>(p.B) * N > INT32_MAX) return AF_ERR_UNSUPPORTED;
+  if (p.D > 16384 || static_cast<int64_t>(p.B) * N > (1 << 30)) return AF_ERR_UNSUPPORTED;
   AF_CUDA(launch_residual_norm(p, dtype == AF_DTYPE_F32, static_cast<cudaStream_t>(stream)));
   return AF_OK;
 }

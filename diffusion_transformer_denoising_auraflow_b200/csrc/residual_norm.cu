@@ -155,11 +155,12 @@ __global__ void __launch_bounds__(1024)
 //   r gate post_weight,   pre_weight (1 + scale),   shift
 // it keeps in shared memory (from the tensors each time they would take three
 // times the row's own bytes); a CTA with one round of rows reads them directly.
-// RING (many rows, whole warps per row): rows stream through a ring of the row
+// Bound: HBM with many rows (three reads and writes of 2 or 4 bytes a value), the
+// launch and one chain of loads and joins with few.
+// RING (many rows with a norm of the branch, whole warps per row): rows stream through a ring of the row
 // group in shared memory, bulk copies issued by its first thread as soon as
 // the group has a row in registers; at 3072 columns seven groups keep two rows
-// each, 168 KB, in flight.  (Without it, loads straight to registers one
-// row ahead, two 9480 x 3072 samples with both norms take 88 us against 80.)
+// each, 168 KB, in flight.
 // Statistics are two-pass; sums are joined by shuffles and, for rows wider
 // than a warp, through shared memory at the row group's named barrier, two
 // buffers in turn so that one barrier per sum is enough.  Packed fp32 pairs.
@@ -255,6 +256,7 @@ struct RnPlan {
   int tg, groups;  // threads per row (a power of two below 32, or whole warps), rows of a CTA at a time
   int per;         // CTAs per sample
   int staged;      // factors in shared memory
+  int fvec;        // their tensors in 16-byte loads
   int stages;      // RING: rows in flight per row group
 };
 // Floats of a plane of the shifted kernel's factors: an entry before and one
@@ -305,6 +307,35 @@ __global__ void __launch_bounds__(RING ? RN_RING_THREADS : 512, V == 1 ? 2 : 1)
       f[1] = rn_pack(lo.z, lo.w);
       f[2] = rn_pack(hi.x, hi.y);
       f[3] = rn_pack(hi.z, hi.w);
+    } else if (plan.fvec) {
+      // eight columns of a vector as packed pairs, or `none` of them
+      auto pairs = [&](const float* v, size_t at, float none, uint64_t (&o)[4]) {
+        float4 lo = make_float4(none, none, none, none), hi = lo;
+        if (v) {
+          lo = __ldg(reinterpret_cast<const float4*>(v + at + c));
+          hi = __ldg(reinterpret_cast<const float4*>(v + at + c + 4));
+        }
+        o[0] = rn_pack(lo.x, lo.y);
+        o[1] = rn_pack(lo.z, lo.w);
+        o[2] = rn_pack(hi.x, hi.y);
+        o[3] = rn_pack(hi.z, hi.w);
+      };
+      uint64_t w[4];
+      if (which == 0) {
+        pairs(p.gate, mo, 1.f, f);
+        pairs(p.post_weight, 0, 1.f, w);
+        const uint64_t r2 = rn_pack(p.residual_scale, p.residual_scale);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = rn_mul2(rn_mul2(r2, f[e]), w[e]);
+      } else if (which == 1) {
+        pairs(p.scale, mo, 0.f, f);
+        pairs(p.pre_weight, 0, 1.f, w);
+        const uint64_t one = rn_pack(1.f, 1.f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = rn_mul2(rn_add2(one, f[e]), w[e]);
+      } else {
+        pairs(p.shift, mo, 0.f, f);
+      }
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -776,8 +807,13 @@ static cudaError_t rn_launch(const ResidualNormParams& p, cudaStream_t s) {
     v = 1;
   } else {
     // many rows: few threads with long rows each (fewer joins, more loads in
-    // flight); fewer rows than SMs: as many threads per row as there are
-    const int cap = static_cast<int64_t>(p.B) * p.rows_per_batch <= sms ? (n8 + 511) / 512 : sizeof(T) == 4 ? 2 : 4;
+    // flight; two 4360 x 3072 samples at 4, 3 and 2 vectors a thread: 39, 47, 60
+    // us); up to two and a half waves of one-vector threads: as many threads per
+    // row as there are (3072 columns, 1, 300, 600 and 1200 rows: 3.8, 6.7, 9.6
+    // and 13.1 us against 5.6, 10.4, 11.4 and 11.1; 1024, 600 and 4096 rows: 4.6
+    // and 12.0 against 6.9 and 11.3)
+    const bool few = static_cast<int64_t>(p.B) * p.rows_per_batch * n8 <= static_cast<int64_t>(2560) * sms;
+    const int cap = few ? (n8 + 511) / 512 : sizeof(T) == 4 ? 2 : 4;
     const int w = (n8 + 32 * cap - 1) / (32 * cap);
     plan.tg = 32 * (w < 16 ? w : 16);
     v = (n8 + plan.tg - 1) / plan.tg;
@@ -793,7 +829,11 @@ static cudaError_t rn_launch(const ResidualNormParams& p, cudaStream_t s) {
   const int one = max(1, sms / p.B);  // CTAs per sample at one per SM
   plan.stages = 0;
   int rounds = split(RN_RING_THREADS);
-  if (v > 1 && rounds > 2 * one) {
+  // The ring where two norms in a row leave loads straight to registers, one row
+  // ahead, too few in flight: two 9480 x 3072 samples 85 us against 98, 2000 rows
+  // 24.4 against 27.6; with the second norm alone it is the other way, 86 against
+  // 81 (fp32, 4360 rows: 81 against 74).
+  if (p.branch && p.post != NORM_NONE && v > 1 && rounds > 2 * one) {
     const int fit = (RN_SMEM_MAX - factor_bytes) / (row_bytes * plan.groups);
     if (fit >= 2) plan.stages = fit < RN_MAX_STAGES ? fit : RN_MAX_STAGES;
   }
@@ -803,15 +843,19 @@ static cudaError_t rn_launch(const ResidualNormParams& p, cudaStream_t s) {
   const int want = ring ? one : max(1, (v == 1 ? 1024 : 512) / threads * sms / p.B);
   plan.per = rounds < want ? rounds : want;
   plan.staged = rounds > plan.per;
+  auto al = [](const void* a) { return (reinterpret_cast<uintptr_t>(a) & 15) == 0; };
+  plan.fvec = al(p.gate) && al(p.scale) && al(p.shift) && al(p.post_weight) && al(p.pre_weight) && p.mod_stride % 4 == 0;
   const unsigned grid = static_cast<unsigned>(p.B) * plan.per;
   const size_t smem =
       (plan.staged ? factor_bytes : 0) + static_cast<size_t>(plan.stages) * plan.groups * row_bytes;
   const bool exact = plan.tg >= 32 && plan.tg * v == n8;
 #define AF_RN_CASE(V_)                                                                                         \
   if (v == V_) {                                                                                               \
-    if (ring)                                                                                                  \
-      return exact ? rn_go<T, OUT8, V_, true, true>(p, plan, grid, threads, smem, s)                            \
-                   : rn_go<T, OUT8, V_, false, true>(p, plan, grid, threads, smem, s);                          \
+    if constexpr (V_ > 1) {                                                                                    \
+      if (ring)                                                                                                \
+        return exact ? rn_go<T, OUT8, V_, true, true>(p, plan, grid, threads, smem, s)                          \
+                     : rn_go<T, OUT8, V_, false, true>(p, plan, grid, threads, smem, s);                        \
+    }                                                                                                          \
     return rn_go<T, OUT8, V_, false, false>(p, plan, grid, threads, smem, s);                                  \
   }
   AF_RN_CASE(1)
@@ -843,7 +887,10 @@ static cudaError_t rn_any(const ResidualNormParams& p, bool aligned, cudaStream_
   const size_t rows = static_cast<size_t>(p.B) * p.rows_per_batch;
   static int sms = 0;
   if (!sms) sms = device_sm_count();
-  // enough rows for every SM to take several: aligned vectors of each row
+  // enough rows for every SM to take more than a round of them: aligned vectors
+  // of each row.  1001 columns, value by value against this (us): 1 row 3.1 and
+  // 5.5, 500 rows 4.0 and 7.1, 1200 rows 6.1 and 7.5, 2400 rows 11.2 and 12.3; 6000
+  // rows of 101 columns 6.8 and 5.5; two 4360 x 3001 samples 102 and 56.
   const int nv = (p.D + 14) / 8;  // vectors that a row may touch
   RnPlan plan{};
   plan.tg = 4;
@@ -855,7 +902,7 @@ static cudaError_t rn_any(const ResidualNormParams& p, bool aligned, cudaStream_
     if (plan.tg > 32 && plan.groups > 15) plan.groups = 15;
     const int one = max(1, sms / p.B), rounds = (p.rows_per_batch + plan.groups - 1) / plan.groups;
     plan.per = rounds < one ? rounds : one;
-    if (rounds >= 2 * one) {
+    if (4 * rounds >= 5 * one) {
       if (v == 1) return rn_shift<T, OUT8, 1>(p, plan, s);
       if (v == 2) return rn_shift<T, OUT8, 2>(p, plan, s);
       if (v == 3) return rn_shift<T, OUT8, 3>(p, plan, s);

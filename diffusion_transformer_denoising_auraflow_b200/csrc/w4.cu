@@ -280,9 +280,9 @@ cudaError_t launch_dequantize_rows_w4(const uint8_t* codes, const uint16_t* scal
 // sum c q - 8 sum q is formed with 8 sum q known per group and column, then
 // multiplied by the group's scale and added up in fp32.
 // Other operands cost more to make: c - 8 in fp16 (x in two pieces) took 77
-// instructions per 16 rows and 64 columns against 50, near the 91 issue slots
+// instructions per 16 rows and 64 columns against 45, near the 91 issue slots
 // that HBM leaves time for; 743424 x 3072 with two rows of x took 218 us
-// against 188-197.
+// against 193 (6.3 TB/s).
 // A row of x that holds an infinity or NaN has no fixed point: its results are
 // summed value by value in fp32 (w4_plain_sum).
 //
@@ -291,15 +291,17 @@ cudaError_t launch_dequantize_rows_w4(const uint8_t* codes, const uint16_t* scal
 // share the columns, in chunks of 256 (128 bytes of codes).  Each warp streams
 // its own 32 rows through its own ring of 4 KB stages: one lane issues the TMA
 // loads of a stage as soon as the warp has read it, so no warp waits for
-// another until a tile's sums are joined.  Rows of a stage are 128-byte lines
+// another until a round's sums are joined.  Rows of a stage are 128-byte lines
 // under the 128-byte swizzle.  A lane (g, t) holds an equal share of a row's
 // group (4, 8 or 16 bytes at G = 32, 64, 128), read by one load; the rows are
 // dealt to g = 0..7 so that each load touches all 32 banks.  Of a word of
-// eight codes, p and p + 4 form one operand register; x lies in shared memory
-// in the order in which the lanes need it.
+// eight codes the even nibbles form one operand register and the odd ones
+// another; x lies in shared memory in that order.
 // Warps of a CTA by the 8-column blocks of x: with more blocks than one the
 // registers of twelve (168 a thread) let 32 rows share the reads of x, and the
-// smaller rings leave shared memory for it.
+// smaller rings leave shared memory for it.  Sixteen warps of 16 rows against
+// twelve of 32: 743424 x 3072 with eight rows of x 305 us and 298, 55296 x 3072
+// with twenty 65 and 62.
 __host__ __device__ constexpr int w4_warps(int nt) { return nt == 1 ? 16 : 12; }
 constexpr int W4_ROWS = 32;                               // rows per warp
 // Rows of a warp whose sums are joined through shared memory at a time.
@@ -309,6 +311,7 @@ constexpr int W4_MAX_NT = 4;                              // 8-column blocks
 constexpr int W4_SMEM_MAX = 227 * 1024;
 constexpr int W4_MAX_STAGES = 4;
 constexpr int W4_MAX_ROWS = W4_MAX_NT * 8 / 3;            // rows of x per CTA, three columns each
+static_assert(W4_MAX_ROWS * 65535 == LINEAR_W4_MAX_M, "a grid's second dimension of CTAs");
 
 struct W4Launch {
   W4Params p;
@@ -703,7 +706,10 @@ cudaError_t launch_linear_w4(const W4Params& p, cudaStream_t s) {
   const bool whole = L.chunks <= room;
   const int per = passes < sms ? sms / passes : 1;  // CTAs per part of x's rows
   // the split with the least time on the busiest SM: rounds of row blocks, each
-  // a chunk time per step, the round's bytes and a fixed end
+  // a chunk time per step, the round's bytes and a fixed end.  Against one warp
+  // per row block (KW = 1): 18432 x 3072, two rows of x, 11.5 us and 18.6;
+  // 3072 x 3072, one row, 4.9 and 16.6; 4099 x 2051, seven rows, 10.8 and 25.5; with
+  // 743424 rows of weights both 199.
   L.blocks = (p.N + rows - 1) / rows;
   float best = 0.f;
   L.rw = 0;
@@ -718,7 +724,7 @@ cudaError_t launch_linear_w4(const W4Params& p, cudaStream_t s) {
       L.rw = rw;
     }
   }
-  if (L.rw == 0 || passes > 65535) return cudaErrorInvalidValue;
+  if (L.rw == 0) return cudaErrorInvalidValue;
   const int kw = warps / L.rw;
   L.seg_chunks = whole ? L.chunks : room / kw * kw;
   L.segs = (L.chunks + L.seg_chunks - 1) / L.seg_chunks;

@@ -412,10 +412,12 @@ af_status af_dequantize_rows_w4(const uint8_t* codes, const uint16_t* scales, in
  * else the identity: the adaLN-Zero modulations W silu(temb) ([ARCH]
  * §联合注意力块) and other projections of a few rows.  f(x) enters as 24-bit
  * fixed point with one factor per row and 256 columns: off by at most 2^-24 of
- * the largest magnitude there (magnitudes below 2^-127 count as zero).
+ * the largest magnitude there (magnitudes below 2^-127, after SiLU 2^-104,
+ * count as zero).
  * Sums of a group are exact, everything else fp32; a row of x with an infinity or
  * NaN is summed term by term in fp32.
- *   x: device [M, K]; out: device [M, N]; bias: device float [N] or NULL.
+ *   x: device [M, K], M at most 655350 (else AF_ERR_UNSUPPORTED); out: device
+ *   [M, N]; bias: device float [N] or NULL.
  * out must not overlap the inputs. */
 af_status af_linear_w4(const void* x, int x_dtype, int silu, const uint8_t* codes, const uint16_t* scales,
                        int scale_stride, const float* bias, void* out, int out_dtype, int M, int N, int K, int group,
@@ -496,7 +498,8 @@ af_status af_ln_modulate(const uint16_t* x, const float* shift, const float* sca
  * post NONE), gate, post_weight, pre_weight (1), shift, scale (0), x_out (x'
  * is not stored), y (no second norm; shift, scale, pre_weight must be NULL),
  * but not both x_out and y.  x_out may be x and y may be branch or x; no
- * other overlap.  D at most 16384 (else AF_ERR_UNSUPPORTED). */
+ * other overlap.  D at most 16384 and B*N at most 2^30 (else
+ * AF_ERR_UNSUPPORTED). */
 #define AF_NORM_NONE 0
 #define AF_NORM_LAYER 1
 #define AF_NORM_RMS 2

@@ -93,6 +93,7 @@ def test_linear_w4_entry_refuses():
     assert _lin(codes=P + 8) == UNSUPPORTED and _lin(scales=P + 2) == UNSUPPORTED
     assert _lin(K=65537) == UNSUPPORTED
     assert _lin(N=(1 << 30) + 8, ss=(1 << 30) + 8) == UNSUPPORTED
+    assert _lin(M=655351) == UNSUPPORTED and _lin(M=2**31 - 1) == UNSUPPORTED  # 65535 CTAs of ten rows of x
 
 
 def test_quantize_entries_refuse():
@@ -126,6 +127,7 @@ def test_residual_norm_entry_refuses():
         assert _rn(y=None, **kw) == INVALID
     assert _rn(D=16385) == UNSUPPORTED
     assert _rn(B=1 << 16, N=1 << 16) == UNSUPPORTED
+    assert _rn(B=2, N=(1 << 29) + 1) == UNSUPPORTED
     e = af.lib.af_residual_norm_e4m3
     assert e(P, P, 0, 1.0, None, None, None, 0, 0, None, 1, None, P, None, P, 1, 1, 8, 1e-6, None) == INVALID
     assert e(P, P, 0, 1.0, None, None, None, 0, 0, None, 1, None, P, P, None, 1, 1, 8, 1e-6, None) == INVALID

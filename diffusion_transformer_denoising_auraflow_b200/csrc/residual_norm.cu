@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(RING ? RN_RING_THREADS : 512, V == 1 ? 2 : 1)
   auto add_of = [&](int d) { return p.shift ? __ldg(p.shift + mo + d) : 0.f; };
   // eight columns of the factors from column c
   auto eight = [&](int which, int c, uint64_t (&f)[4]) {
-    if (plan.staged) {
+    if (RING || plan.staged) {  // a ring has more rows than CTAs
       const float4 lo = *reinterpret_cast<const float4*>(factors + which * D + c / 2);
       const float4 hi = *reinterpret_cast<const float4*>(factors + which * D + D / 2 + c / 2);
       f[0] = rn_pack(lo.x, lo.y);
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(RING ? RN_RING_THREADS : 512, V == 1 ? 2 : 1)
     if (p.branch) bulk_load(dst + row_bytes, static_cast<const T*>(p.branch) + at, row_bytes, bar);
   };
   if constexpr (RING) {
-    ring = smem_u32(factors) + (plan.staged ? D * 12 : 0) + grp * plan.stages * stage_bytes;
+    ring = smem_u32(factors) + D * 12 + grp * plan.stages * stage_bytes;
     if (threadIdx.x == 0) abort_flag = 0;
     if (tid == 0) {
       for (int i = 0; i < plan.stages; ++i) mbar_init(smem_u32(&full[grp][i]), 1);
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(RING ? RN_RING_THREADS : 512, V == 1 ? 2 : 1)
   } else {
     fetch(r);
   }
-  if (plan.staged) {
+  if (RING || plan.staged) {
     for (int d = 4 * threadIdx.x; d < D; d += 4 * blockDim.x) {  // four columns: their loads overlap
       const int at = (d & 4 ? D / 2 : 0) + (d >> 3) * 4;
       float f[3][4];
@@ -830,9 +830,9 @@ static cudaError_t rn_launch(const ResidualNormParams& p, cudaStream_t s) {
   plan.stages = 0;
   int rounds = split(RN_RING_THREADS);
   // The ring where two norms in a row leave loads straight to registers, one row
-  // ahead, too few in flight: two 9480 x 3072 samples 85 us against 98, 2000 rows
-  // 24.4 against 27.6; with the second norm alone it is the other way, 86 against
-  // 81 (fp32, 4360 rows: 81 against 74).
+  // ahead, too few in flight: two 9480 x 3072 samples 81 us against 98, two of 2000
+  // rows 23.5 against 27.6; with the second norm alone it is the other way, 91
+  // against 81 (4360 rows 41.5 against 41.1, in fp32 77 against 74).
   if (p.branch && p.post != NORM_NONE && v > 1 && rounds > 2 * one) {
     const int fit = (RN_SMEM_MAX - factor_bytes) / (row_bytes * plan.groups);
     if (fit >= 2) plan.stages = fit < RN_MAX_STAGES ? fit : RN_MAX_STAGES;

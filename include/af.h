@@ -430,8 +430,10 @@ af_status af_linear_w4(const void* x, int x_dtype, int silu, const uint8_t* code
  * on `w` compute its modulations from it with af_linear_w4 (silu(temb) in
  * fp32).  bf16 and fp32 packs, with or without the 8-bit projections.  Call it
  * again after changing weights; group = 0 frees the copy and returns to the
- * pack's own weights.  Work on `w` in flight must have ended when the copy is
- * freed or re-made with another group. */
+ * pack's own weights.  The quantiser runs on `stream`: work on `w` on other
+ * streams waits for it or has ended.  When the copy is freed or re-made with
+ * another group, work on `w` in flight must have ended, and graphs captured
+ * from calls on `w` since it was made are not replayed any more. */
 af_status af_weights_quantize_w4(af_weights* w, int group, void* stream);
 
 /* Host-side sigma schedule of the flow-match Euler sampler ([DEEP] §2.3:

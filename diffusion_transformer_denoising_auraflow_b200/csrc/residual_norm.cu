@@ -779,16 +779,16 @@ __global__ void __launch_bounds__(512, 1)
 template <typename T, bool OUT8, int V, bool EXACT, bool RING>
 static cudaError_t rn_go(const ResidualNormParams& p, const RnPlan& plan, unsigned grid, int threads, size_t smem,
                          cudaStream_t s) {
+  // The opt-in at every size: what launches without it is 48 KB less the kernel's
+  // own arrays (2 KB of sums), which the factors alone reach at 3944 columns.
   static uint64_t done = 0;  // one bit per device: the kernel's shared-memory opt-in
-  if (smem > 48 * 1024) {
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (!((done >> dev) & 1u)) {
-      const cudaError_t e = cudaFuncSetAttribute(residual_norm_kernel<T, OUT8, V, EXACT, RING>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, RN_SMEM_MAX);
-      if (e != cudaSuccess) return e;
-      done |= uint64_t(1) << dev;
-    }
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (!((done >> dev) & 1u)) {
+    const cudaError_t e = cudaFuncSetAttribute(residual_norm_kernel<T, OUT8, V, EXACT, RING>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, RN_SMEM_MAX);
+    if (e != cudaSuccess) return e;
+    done |= uint64_t(1) << dev;
   }
   residual_norm_kernel<T, OUT8, V, EXACT, RING><<<grid, threads, smem, s>>>(p, plan);
   return cudaGetLastError();

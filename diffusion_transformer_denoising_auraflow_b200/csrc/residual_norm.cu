@@ -475,6 +475,7 @@ __global__ void __launch_bounds__(RING ? RN_RING_THREADS : 512, V == 1 ? 2 : 1)
       uint32_t failed;
       if (warps == 1) {
         failed = __any_sync(0xffffffffu, !got);
+        __syncwarp();  // the vote alone does not order the lanes' reads before the next copy
       } else {
         asm volatile(
             "{\n\t.reg .pred p, q;\n\t"

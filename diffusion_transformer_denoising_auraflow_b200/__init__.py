@@ -864,7 +864,8 @@ def residual_norm(x, branch, x_out, y, eps: float, gate=None, shift=None, scale=
 def residual_norm_e4m3(x, branch, x_out, y8, yscale, eps: float, gate=None, shift=None, scale=None,
                        mod_stride: int = 0, residual_scale: float = 1.0, post: str = "none", post_weight=None,
                        pre: str = "layer", pre_weight=None, stream=None):
-    """residual_norm with y as e4m3 codes y8 (uint8, B * N rows of D) and fp32 row scales yscale."""
+    """residual_norm with y as e4m3 codes y8 (uint8, B * N rows of D) and fp32 row scales yscale;
+    neither may share memory with another tensor of the call."""
     where = "af_residual_norm_e4m3"
     B, N, D = x.shape
     _dtype_code(x, "x")

@@ -1805,6 +1805,12 @@ af_status af_linear_w4(const void* x, int x_dtype, int silu, const uint8_t* code
   return AF_OK;
 }
 
+// Whether n bytes at a and m bytes at b share a byte; nothing does with NULL.
+static bool overlap(const void* a, size_t n, const void* b, size_t m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + m && y < x + n;
+}
+
 static af_status residual_norm_call(ResidualNormParams p, int dtype, int N, void* stream) {
   if (!p.x || (!p.x_out && !p.y) || !is_dtype(dtype)) return AF_ERR_INVALID_ARG;
   if (p.B <= 0 || N <= 0 || p.D <= 0 || p.mod_stride < 0 || !(p.eps >= 0.f)) return AF_ERR_INVALID_ARG;
@@ -1812,6 +1818,13 @@ static af_status residual_norm_call(ResidualNormParams p, int dtype, int N, void
   if (!p.branch && (p.gate || p.post_weight || p.post != NORM_NONE)) return AF_ERR_INVALID_ARG;
   if (!p.y && (p.shift || p.scale || p.pre_weight)) return AF_ERR_INVALID_ARG;
   if (p.D > 16384 || static_cast<int64_t>(p.B) * N > (1 << 30)) return AF_ERR_UNSUPPORTED;
+  if (p.yscale) {  // codes are not as wide as the rows they come from: over a row they would meet others still unread
+    const size_t rows = static_cast<size_t>(p.B) * N, wide = rows * p.D * (dtype == AF_DTYPE_F32 ? 4 : 2);
+    const void* tensors[] = {p.x, p.branch, p.x_out};
+    for (const void* t : tensors)
+      if (overlap(p.y, rows * p.D, t, wide) || overlap(p.yscale, rows * 4, t, wide)) return AF_ERR_INVALID_ARG;
+    if (overlap(p.y, rows * p.D, p.yscale, rows * 4)) return AF_ERR_INVALID_ARG;
+  }
   AF_CUDA(launch_residual_norm(p, dtype == AF_DTYPE_F32, static_cast<cudaStream_t>(stream)));
   return AF_OK;
 }

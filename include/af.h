@@ -512,7 +512,9 @@ af_status af_residual_norm(const void* x, const void* branch, int dtype, float r
 
 /* The same with y as e4m3 codes y8 (device uint8 [B*N, D]) and row scales
  * yscale (device float [B*N]), with the rule of af_quantize_rows_e4m3 applied
- * to the fp32 y: the input of af_linear_fp8. */
+ * to the fp32 y: the input of af_linear_fp8.  x_out may be x; y8 and yscale
+ * overlap nothing (a row's codes would lie over other rows): with x, branch,
+ * x_out or each other that is AF_ERR_INVALID_ARG. */
 af_status af_residual_norm_e4m3(const void* x, const void* branch, int dtype, float residual_scale, const float* gate,
                                 const float* shift, const float* scale, int mod_stride, int post,
                                 const float* post_weight, int pre, const float* pre_weight, void* x_out, uint8_t* y8,

@@ -737,6 +737,10 @@ def _ptr_rows(t, dtype, name: str, where: str, dev: int, rows: int, row_stride: 
             return t.data_ptr()
     if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
         raise AFError(AF_ERR_SHAPE, where, f"{name} must be contiguous along its last axis")
+    if (t.dim() >= 2 and rows > 1 and t.shape[0] == rows and t.shape[-1] == row_len and t.numel() == rows * row_len
+            and t.stride(0) != row_stride):  # a vector per sample, of which the call would read others
+        raise AFError(AF_ERR_SHAPE, where,
+                      f"{name} has its {rows} rows {t.stride(0)} elements apart, but mod_stride is {row_stride}")
     _dev_rows(t, dtype, name, rows, row_stride, row_len, where)
     return _on_device(t, name, where, dev)
 
@@ -846,7 +850,8 @@ def residual_norm(x, branch, x_out, y, eps: float, gate=None, shift=None, scale=
     """x' = x + residual_scale * gate * post(branch) * post_weight into x_out and
     y = pre(x') * pre_weight * (1 + scale) + shift into y, in one pass over the
     rows of x [B, N, D] (bf16 or fp32).  post and pre: "none", "layer" or "rms".
-    gate, shift, scale: fp32, sample b's vector at element b * mod_stride.
+    gate, shift, scale: fp32, sample b's vector at element b * mod_stride; 0 is
+    one vector [D] for all samples, a [B, D] tensor needs its row stride there.
     branch, x_out or y may be None (see af_residual_norm)."""
     where = "af_residual_norm"
     B, N, D = x.shape

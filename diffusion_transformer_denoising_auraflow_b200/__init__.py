@@ -694,6 +694,7 @@ def linear_fp8(A8, a_scale, W8, w_scale, C, stream=None):
 # Calls of a few microseconds on the device: a tensor that is as it should be
 # costs one condition here, the messages are made where one is not.
 
+_T = torch.Tensor
 _DTYPE_CODE = {torch.bfloat16: AF_DTYPE_BF16, torch.float32: AF_DTYPE_F32}
 
 
@@ -703,6 +704,12 @@ def _dtype_code(t, name: str) -> int:
     if code is None:
         raise TypeError(f"{name} must be a bfloat16 or float32 tensor")
     return code
+
+
+def _need_tensors(**named):
+    for name, t in named.items():
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a CUDA tensor, got {type(t).__name__}")
 
 
 def _current(t) -> int:
@@ -776,6 +783,8 @@ def _w4_args(codes, scales, N: int, K: int, group: int, where: str, dev: int):
 def quantize_rows_w4(w, group: int, codes, scales, stream=None):
     """4-bit codes and group scales of w [N, K] (bf16 or fp32) into codes and scales (shapes: w4_shapes)."""
     where = "af_quantize_rows_w4"
+    if not (isinstance(w, _T) and isinstance(codes, _T) and isinstance(scales, _T)):
+        _need_tensors(w=w, codes=codes, scales=scales)
     N, K = w.shape
     dt = _dtype_code(w, "w")
     dev = _current(w)
@@ -789,6 +798,8 @@ def quantize_rows_w4(w, group: int, codes, scales, stream=None):
 def dequantize_rows_w4(codes, scales, group: int, out, stream=None):
     """The values of 4-bit codes and scales into out [N, K] (bf16 or fp32)."""
     where = "af_dequantize_rows_w4"
+    if not (isinstance(codes, _T) and isinstance(scales, _T) and isinstance(out, _T)):
+        _need_tensors(codes=codes, scales=scales, out=out)
     N, K = out.shape
     dt = _dtype_code(out, "out")
     dev = _current(out)
@@ -803,6 +814,8 @@ def linear_w4(x, codes, scales, group: int, out, silu: bool = False, bias=None, 
     """out [M, N] = f(x [M, K]) W^T + bias with W in 4 bits; f is SiLU or the
     identity; x and out bf16 or fp32, bias fp32 [N] or None."""
     where = "af_linear_w4"
+    if not (isinstance(x, _T) and isinstance(codes, _T) and isinstance(scales, _T) and isinstance(out, _T)):
+        _need_tensors(x=x, codes=codes, scales=scales, out=out)
     M, K = x.shape
     N = codes.shape[0]
     if out.shape != (M, N):
@@ -854,6 +867,8 @@ def residual_norm(x, branch, x_out, y, eps: float, gate=None, shift=None, scale=
     one vector [D] for all samples, a [B, D] tensor needs its row stride there.
     branch, x_out or y may be None (see af_residual_norm)."""
     where = "af_residual_norm"
+    if not isinstance(x, _T):
+        _need_tensors(x=x)
     B, N, D = x.shape
     _dtype_code(x, "x")
     if y is not None and y.shape != x.shape:
@@ -872,6 +887,8 @@ def residual_norm_e4m3(x, branch, x_out, y8, yscale, eps: float, gate=None, shif
     """residual_norm with y as e4m3 codes y8 (uint8, B * N rows of D) and fp32 row scales yscale;
     neither may share memory with another tensor of the call."""
     where = "af_residual_norm_e4m3"
+    if not (isinstance(x, _T) and isinstance(y8, _T) and isinstance(yscale, _T)):
+        _need_tensors(x=x, y8=y8, yscale=yscale)
     B, N, D = x.shape
     _dtype_code(x, "x")
     if y8.numel() != B * N * D:

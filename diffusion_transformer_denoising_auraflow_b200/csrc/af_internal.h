@@ -156,7 +156,7 @@ cudaError_t launch_convert_copy(const void* src, bool src_f32, void* dst, bool d
 
 // Weights in 4 bits with group scales (w4.cu).  codes [N, ceil(K / group) *
 // group / 2], scales bf16 [ceil(K / group), scale_stride].
-constexpr int LINEAR_W4_MAX_M = 10 * 65535;  // rows of x: ten per CTA
+constexpr int LINEAR_W4_MAX_M = 655350;
 struct W4Params {
   const void* x;         // [M, K], bf16 or fp32 (x_f32)
   const uint8_t* codes;

@@ -43,6 +43,8 @@ __device__ __forceinline__ uint64_t w4_fma2(uint64_t a, uint64_t b, uint64_t c) 
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
+__device__ __forceinline__ float w4_lo(uint64_t a) { return __uint_as_float(static_cast<uint32_t>(a)); }
+__device__ __forceinline__ float w4_hi(uint64_t a) { return __uint_as_float(static_cast<uint32_t>(a >> 32)); }
 constexpr float W4_MAGIC = 12582912.0f;    // 1.5 * 2^23: the bits of W4_MAGIC + i are its bits + i for |i| < 2^22
 
 // Eight columns of a row from column k as stored (bf16 in the first vector,
@@ -273,12 +275,16 @@ cudaError_t launch_dequantize_rows_w4(const uint8_t* codes, const uint16_t* scal
 //
 // Each group's sum runs on mma.sync m16n8k32 in whole numbers: the weights are
 // the 16-row operand, the codes c as they are (two masks and a shift unpack
-// eight), the columns are rows of x as 24-bit fixed point, cut into three
-// signed bytes, a column each.  One factor per row of x and 256 columns takes
-// the largest magnitude a there to +-8355000, so a value is off by at most
-// a 2^-24, half an fp32 step of a.  Sums are exact (at most 15 * 128 * 128);
-// sum c q - 8 sum q is formed with 8 sum q known per group and column, then
-// multiplied by the group's scale and added up in fp32.
+// eight), the columns are rows of x as 32-bit fixed point, cut into four
+// signed bytes, a column each.  The step per row of x and 256 columns is a power
+// of two, at most 2^-30 (1 + 2^-7) of the largest magnitude a there: a value of
+// at least a 2^-6 enters exactly, any other off by at most half a step.  Three
+// bytes (24 bits) leave values next to a far larger one with too few bits,
+// which shows where the larger one meets a zero weight; the fourth costs
+// nothing at one and two rows of x (eight columns are one operand).
+// Sums are exact (at most 15 * 128 * 128); sum c q - 8 sum q is formed with
+// 8 sum q known per group and column, then multiplied by the group's scale and
+// added up in fp32.
 // Other operands cost more to make: c - 8 in fp16 (x in two pieces) took 77
 // instructions per 16 rows and 64 columns against 45, near the 91 issue slots
 // that HBM leaves time for; 743424 x 3072 with two rows of x took 218 us
@@ -299,19 +305,23 @@ cudaError_t launch_dequantize_rows_w4(const uint8_t* codes, const uint16_t* scal
 // another; x lies in shared memory in that order.
 // Warps of a CTA by the 8-column blocks of x: with more blocks than one the
 // registers of twelve (168 a thread) let 32 rows share the reads of x, and the
-// smaller rings leave shared memory for it.  Sixteen warps of 16 rows against
-// twelve of 32: 743424 x 3072 with eight rows of x 305 us and 298, 55296 x 3072
-// with twenty 65 and 62.
+// smaller rings leave shared memory for it.  With three columns a row of x,
+// sixteen warps of 16 rows against twelve of 32: 743424 x 3072 with eight rows of
+// x 305 us and 298, 55296 x 3072 with twenty 65 and 62.  Four columns against
+// three, 120000 x 3072 with 2, 4, 8, 10 and 32 rows: 38, 49, 75, 99 and 238 us against
+// 38, 50, 63, 165 (x in parts) and 185.
 __host__ __device__ constexpr int w4_warps(int nt) { return nt == 1 ? 16 : 12; }
 constexpr int W4_ROWS = 32;                               // rows per warp
-// Rows of a warp whose sums are joined through shared memory at a time.
+// Rows of a warp whose sums are joined through shared memory at a time, and the
+// floats between rows of x there (16 mod 32: two of them fill the banks).
 __host__ __device__ constexpr int w4_red_rows(int nt) { return nt == 1 ? W4_ROWS : 16; }
+__host__ __device__ constexpr int w4_red_pitch(int nt) { return nt == 1 ? 48 : 16; }
 constexpr int W4_CHUNK = 256;                             // columns per chunk
 constexpr int W4_MAX_NT = 4;                              // 8-column blocks
 constexpr int W4_SMEM_MAX = 227 * 1024;
 constexpr int W4_MAX_STAGES = 4;
-constexpr int W4_MAX_ROWS = W4_MAX_NT * 8 / 3;            // rows of x per CTA, three columns each
-static_assert(W4_MAX_ROWS * 65535 == LINEAR_W4_MAX_M, "a grid's second dimension of CTAs");
+constexpr int W4_DIGITS = 4;                              // columns of a row of x, two neighbouring lanes' of a block
+constexpr int W4_MAX_ROWS = W4_MAX_NT * 8 / W4_DIGITS;    // rows of x per CTA
 
 struct W4Launch {
   W4Params p;
@@ -322,8 +332,10 @@ struct W4Launch {
   int x_vec;                // x in 16-byte loads: aligned, K a multiple of 8
 };
 
-constexpr float W4_FIX = 8355000.0f;       // largest fixed-point value; three signed bytes reach 8355711
-constexpr float W4_TINY = 0x1p-104f;       // a row's chunk below this counts in steps of W4_TINY / W4_FIX
+// Fixed point: a (1 + 2^-7) < 2^(e + 1) counts in steps of 2^(e - 30), so that
+// a's number is below 2^31 / (1 + 2^-7) = 2130836295; four signed bytes reach
+// 2139062143.  e is kept so that the step is no smaller than fp32's smallest, 2^-149.
+constexpr float W4_SMALL = 0x1p-90f;       // where the largest is below this, scaled by 2^24 first
 constexpr int W4_MAGIC_BITS = 0x4B400000;
 
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
@@ -395,7 +407,7 @@ __device__ __forceinline__ void w4_stage_x(const W4Launch& L, int m0, int rows, 
     const W4Raw raw = next;
     next = load(i + W);
     const int m = i / chunks, c = i - m * chunks;
-    float v[8], a = W4_TINY;
+    float v[8], a = 0.f;
     w4_values(raw, p.x_f32, v);
     bool fine = true;
 #pragma unroll
@@ -406,20 +418,29 @@ __device__ __forceinline__ void w4_stage_x(const W4Launch& L, int m0, int rows, 
     }
     asm volatile("redux.sync.max.abs.f32 %0, %0, 0xffffffff;" : "+f"(a));
     if (!fine) bad[m] = 1;
-    const float up = __fdiv_rn(W4_FIX, a), down = __fdiv_rn(1.0f, up);
-    uint32_t f[8];  // three signed bytes each: q = d0 + 256 d1 + 65536 d2
+    const bool small = a < W4_SMALL;
+    if (small) {
+      a *= 0x1p24f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= 0x1p24f;
+    }
+    // biased e: 32 at least, which after the 2^24 is a step of 2^-149
+    const int exp = max(static_cast<int>(__float_as_uint(fmaf(a, 0x1p-7f, a)) >> 23), 32);
+    const float up = __uint_as_float(static_cast<uint32_t>(284 - exp) << 23);
+    const float down = __uint_as_float(static_cast<uint32_t>(exp - 30) << 23) * (small ? 0x1p-24f : 1.0f);
+    uint32_t f[8];  // four signed bytes each: q = d0 + 256 d1 + 65536 d2 + 16777216 d3
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      f[e] = (static_cast<uint32_t>(__float2int_rn(v[e] * up)) + 0x808080u) ^ 0x808080u;
+      f[e] = (static_cast<uint32_t>(__float2int_rn(v[e] * up)) + 0x80808080u) ^ 0x80808080u;
 #pragma unroll
-    for (int d = 0; d < 3; ++d) {
+    for (int d = 0; d < W4_DIGITS; ++d) {
       const uint32_t sel = 0x40u + 0x11u * d;  // byte d of both
       const uint32_t lo = __byte_perm(__byte_perm(f[0], f[2], sel), __byte_perm(f[4], f[6], sel), 0x5410);
       const uint32_t hi = __byte_perm(__byte_perm(f[1], f[3], sel), __byte_perm(f[5], f[7], sel), 0x5410);
       int sum = __dp4a(static_cast<int>(lo), 0x01010101, __dp4a(static_cast<int>(hi), 0x01010101, 0));
 #pragma unroll
       for (int o = G / 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      const int col = 3 * m + d;
+      const int col = W4_DIGITS * m + d;
       asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(X.x + col * L.x_pitch + 8 * (c * 32 + lane)), "r"(lo),
                    "r"(hi)
                    : "memory");
@@ -454,7 +475,8 @@ __global__ void __launch_bounds__(32 * w4_warps(NT), 1)
   constexpr int W = w4_warps(NT), THREADS = 32 * W;
   constexpr int ROWS = W4_ROWS, H = ROWS / 16;       // rows per warp, 16-row operands
   constexpr int STAGE = ROWS * W4_CHUNK / 2;         // code bytes per stage
-  constexpr int RED = w4_red_rows(NT), RED_LD = RED + 4;  // rows of a warp joined at a time; floats between columns
+  constexpr int RED = w4_red_rows(NT), RED_LD = w4_red_pitch(NT);
+  constexpr int XR = NT * 8 / W4_DIGITS;             // rows of x of the columns
   __shared__ uint64_t full[W][W4_MAX_STAGES];
   __shared__ int abort_flag, bad[W4_MAX_ROWS];
   constexpr int GPC = W4_CHUNK / G;              // groups per chunk
@@ -468,10 +490,10 @@ __global__ void __launch_bounds__(32 * w4_warps(NT), 1)
   const uint32_t codes_s = base + warp * L.stages * STAGE;
   const uint32_t sc_s = base + W * L.stages * STAGE + warp * L.stages * SC_STAGE;
   const uint32_t red_base = base + W * L.stages * (STAGE + SC_STAGE);
-  const int m0 = blockIdx.y * L.rows_m, rows = min(L.rows_m, p.M - m0), cols = 3 * rows;
+  const int m0 = blockIdx.y * L.rows_m, rows = min(L.rows_m, p.M - m0), cols = W4_DIGITS * rows;
   W4X X;
-  X.x = red_base + W * NT * 8 * RED_LD * 4;
-  X.fac = X.x + 3 * L.rows_m * L.x_pitch;
+  X.x = red_base + W * XR * RED_LD * 4;
+  X.fac = X.x + W4_DIGITS * L.rows_m * L.x_pitch;
   X.off = X.fac + L.seg_chunks * NT * 32;
   if (threadIdx.x < W4_MAX_ROWS) bad[threadIdx.x] = 0;
   if (threadIdx.x == 0) abort_flag = 0;
@@ -516,7 +538,7 @@ __global__ void __launch_bounds__(32 * w4_warps(NT), 1)
   for (int i = 0; i < NT; ++i) xcol[i] = X.x + min(8 * i + g, cols - 1) * L.x_pitch + 8 * WORDS * t;
   // this lane's bytes of group 0 in row r8 of a stage; group gi is at ^ (gi * 16 * WORDS)
   const uint32_t mine = r8 * 128 + ((((WORDS * t) >> 2) ^ r8) << 4) + 4 * ((WORDS * t) & 3);
-  const uint32_t red = red_base + warp * NT * 8 * RED_LD * 4;
+  const uint32_t red = red_base + warp * XR * RED_LD * 4;
   int4 magic;  // four registers of their own: the first sum of a group starts from them
   asm volatile("mov.b32 %0, %4; mov.b32 %1, %4; mov.b32 %2, %4; mov.b32 %3, %4;"
                : "=r"(magic.x), "=r"(magic.y), "=r"(magic.z), "=r"(magic.w)
@@ -531,11 +553,11 @@ __global__ void __launch_bounds__(32 * w4_warps(NT), 1)
   }
   for (int round = 0; round * round_blocks < L.blocks; ++round) {
     const int block = first_block + round * round_blocks;
-    uint64_t acc[H][NT][2];  // pairs of columns, rows r8 and r8 + 8
+    float acc[H][NT][2];  // this lane's two digits of a row of x together; rows r8 and r8 + 8
 #pragma unroll
     for (int h = 0; h < H; ++h)
 #pragma unroll
-      for (int i = 0; i < NT; ++i) acc[h][i][0] = acc[h][i][1] = 0;
+      for (int i = 0; i < NT; ++i) acc[h][i][0] = acc[h][i][1] = 0.f;
     int xc = kw;  // the chunk's place in the part of x at hand
     for (int chunk = 0; chunk < L.chunks; chunk += kw_n, xc += kw_n) {
       if (L.segs > 1 && chunk % L.seg_chunks == 0) {  // x does not fit whole: its next part
@@ -604,7 +626,8 @@ __global__ void __launch_bounds__(32 * w4_warps(NT), 1)
 #pragma unroll
           for (int h = 0; h < H; ++h) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) acc[h][i][e] = w4_fma2(f, part[h][i][e], acc[h][i][e]);
+            for (int e = 0; e < 2; ++e)
+              acc[h][i][e] = fmaf(w4_hi(f), w4_hi(part[h][i][e]), fmaf(w4_lo(f), w4_lo(part[h][i][e]), acc[h][i][e]));
           }
         }
         __syncwarp();
@@ -615,7 +638,8 @@ __global__ void __launch_bounds__(32 * w4_warps(NT), 1)
         ph ^= 1u;
       }
     }
-    // the round's sums, RED rows of each warp at a time: by columns, then over the KW warps and the pieces of a row of x
+    // the round's sums, RED rows of each warp at a time: the neighbouring lanes' halves of a row of x, then
+    // over the KW warps
 #pragma unroll
     for (int h0 = 0; h0 < H; h0 += RED / 16) {
       if (kw_n > 1) __syncthreads();  // the last ones are read
@@ -623,13 +647,11 @@ __global__ void __launch_bounds__(32 * w4_warps(NT), 1)
 #pragma unroll
       for (int h = 0; h < RED / 16; ++h)
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          const uint32_t a = red + ((8 * i + 2 * t) * RED_LD + 16 * h + r8) * 4;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            sts_f1(a + 32 * e, __uint_as_float(static_cast<uint32_t>(acc[h0 + h][i][e])));
-            sts_f1(a + 32 * e + RED_LD * 4, __uint_as_float(static_cast<uint32_t>(acc[h0 + h][i][e] >> 32)));
-          }
+        for (int i = 0; i < NT; ++i) {  // even lanes finish row r8, odd ones r8 + 8
+          const float a0 = acc[h0 + h][i][0], a1 = acc[h0 + h][i][1];
+          const bool odd = t & 1;
+          const float v = (odd ? a1 : a0) + __shfl_xor_sync(0xffffffffu, odd ? a0 : a1, 1);
+          sts_f1(red + ((2 * i + (t >> 1)) * RED_LD + 16 * h + r8 + 8 * (t & 1)) * 4, v);
         }
       if (kw_n > 1) __syncthreads();
       else __syncwarp();
@@ -640,11 +662,9 @@ __global__ void __launch_bounds__(32 * w4_warps(NT), 1)
         if (bad[m]) {
           v = w4_plain_sum(p, m0 + m, n);
         } else {
-          const uint32_t at = red_base + ((from * NT * 8 + 3 * m) * RED_LD + r) * 4;
+          const uint32_t at = red_base + ((from * XR + m) * RED_LD + r) * 4;
           for (int k = 0; k < kw_n && k < L.chunks; ++k)
-#pragma unroll
-            for (int d = 0; d < 3; ++d)
-              v += __uint_as_float(lds32(at + (k * rw_n * NT * 8 + d) * RED_LD * 4));
+            v += __uint_as_float(lds32(at + k * rw_n * XR * RED_LD * 4));
         }
         if (p.bias) v += p.bias[n];
         w4_store(p.out, p.out_f32, static_cast<size_t>(m0 + m) * p.out_stride + n, v);
@@ -683,7 +703,18 @@ static cudaError_t linear_w4_launch(const W4Launch& L, const CUtensorMap& tc, co
   return cudaGetLastError();
 }
 
-cudaError_t launch_linear_w4(const W4Params& p, cudaStream_t s) {
+cudaError_t launch_linear_w4(const W4Params& whole_p, cudaStream_t s) {
+  W4Params p = whole_p;
+  constexpr int MOST = W4_MAX_ROWS * 65535;  // a grid's second dimension of CTAs
+  if (p.M > MOST) {  // the rows behind them by a launch of their own
+    p.M -= MOST;
+    p.x = static_cast<const uint8_t*>(p.x) + static_cast<size_t>(MOST) * p.K * (p.x_f32 ? 4 : 2);
+    p.out = static_cast<uint8_t*>(p.out) + MOST * p.out_stride * (p.out_f32 ? 4 : 2);
+    const cudaError_t e = launch_linear_w4(p, s);
+    if (e != cudaSuccess) return e;
+    p = whole_p;
+    p.M = MOST;
+  }
   static int sms = 0;
   if (!sms) sms = device_sm_count();
   const int groups = (p.K + p.group - 1) / p.group;
@@ -694,9 +725,9 @@ cudaError_t launch_linear_w4(const W4Params& p, cudaStream_t s) {
   L.x_vec = w4_vec(p.x, p.K);
   const int passes = (p.M + W4_MAX_ROWS - 1) / W4_MAX_ROWS;
   L.rows_m = (p.M + passes - 1) / passes;
-  const int cols = 3 * L.rows_m, nt = (cols + 7) / 8, warps = w4_warps(nt), rows = W4_ROWS;
+  const int cols = W4_DIGITS * L.rows_m, nt = (cols + 7) / 8, warps = w4_warps(nt), rows = W4_ROWS;
   const int stage = warps * (rows * W4_CHUNK / 2 + rows * (W4_CHUNK / p.group) * 2);
-  const int fixed = warps * nt * 8 * (w4_red_rows(nt) + 4) * 4 + 3072;  // sums, alignment, static barriers
+  const int fixed = warps * nt * 8 / W4_DIGITS * w4_red_pitch(nt) * 4 + 3072;  // sums, alignment, static barriers
   // x lies in shared memory whole if two stages fit beside it, else in parts
   // of `seg` chunks, a multiple of the chunks that share a row; columns are
   // spaced so that the lanes of a bank cycle differ

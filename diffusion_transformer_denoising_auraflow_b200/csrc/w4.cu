@@ -27,6 +27,13 @@ __device__ __forceinline__ float w4_bf16(uint16_t b) { return __uint_as_float(st
 // exp and division to a few last bits (2 + 1.2 |a| and 2): a third of the instructions of expf and a true division
 __device__ __forceinline__ float w4_silu(float a) { return __fdividef(a, 1.0f + __expf(-a)); }
 
+// the larger one, NaN if either is
+__device__ __forceinline__ float w4_max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 // packed fp32 pairs
 __device__ __forceinline__ uint64_t w4_pack2(float a, float b) {
   uint64_t r;
@@ -289,8 +296,15 @@ cudaError_t launch_dequantize_rows_w4(const uint8_t* codes, const uint16_t* scal
 // instructions per 16 rows and 64 columns against 45, near the 91 issue slots
 // that HBM leaves time for; 743424 x 3072 with two rows of x took 218 us
 // against 193 (6.3 TB/s).
-// A row of x that holds an infinity or NaN has no fixed point: its results are
-// summed value by value in fp32 (w4_plain_sum).
+// One step does not fit 256 columns of which most are far below the largest:
+// the others' last bits show in weights that are zero at the few large ones.
+// Where fewer than four, or than one in 16, of the values other than zero reach
+// 2^-10 of the largest, these are set aside (W4_FAR a row at most, in the order of
+// their columns) and added as fp32 terms of their own to the finished sums; the
+// step is that of the rest.  A row with more of them, an infinity or a NaN is
+// summed term by term in fp32 (w4_plain_sum).  18432 x 3072 with a value set aside in each of one row
+// and of seven: 10.3 us and 24 against 9.2 and 18.5; one row and seven summed term by
+// term 143 and 633.
 //
 // Bound: the code bytes from HBM (4.25 bits a weight at G = 64).  One CTA of W
 // warps per SM, RW x KW of them: RW blocks of 32 rows by KW ways to
@@ -319,6 +333,7 @@ __host__ __device__ constexpr int w4_red_pitch(int nt) { return nt == 1 ? 48 : 1
 constexpr int W4_CHUNK = 256;                             // columns per chunk
 constexpr int W4_MAX_NT = 4;                              // 8-column blocks
 constexpr int W4_SMEM_MAX = 227 * 1024;
+constexpr int W4_STATIC = 4096;                           // of it the barriers and values set aside, and spare
 constexpr int W4_MAX_STAGES = 4;
 constexpr int W4_DIGITS = 4;                              // columns of a row of x, two neighbouring lanes' of a block
 constexpr int W4_MAX_ROWS = W4_MAX_NT * 8 / W4_DIGITS;    // rows of x per CTA
@@ -335,6 +350,8 @@ struct W4Launch {
 // Fixed point: a (1 + 2^-7) < 2^(e + 1) counts in steps of 2^(e - 30), so that
 // a's number is below 2^31 / (1 + 2^-7) = 2130836295; four signed bytes reach
 // 2139062143.  e is kept so that the step is no smaller than fp32's smallest, 2^-149.
+constexpr int W4_FAR = 32;                                // values set aside a row, a warp's lanes
+constexpr int W4_NOT_FINITE = 1 << 30;                    // their count where the row has an infinity or NaN
 constexpr float W4_SMALL = 0x1p-90f;       // where the largest is below this, scaled by 2^24 first
 constexpr int W4_MAGIC_BITS = 0x4B400000;
 
@@ -364,15 +381,63 @@ __device__ __forceinline__ void mma_16832(int (&d)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(c0), "r"(c1), "r"(c2), "r"(c3));
 }
 
-// sum_k f(x[m, k]) value(n, k) term by term, for rows of x that are not finite.
-__device__ __noinline__ float w4_plain_sum(const W4Params& p, int m, int n) {
-  const uint8_t* cr = p.codes + static_cast<size_t>(n) * ((p.K + p.group - 1) / p.group) * (p.group / 2);
+// sum_k f(x[m, k]) value(n, k) term by term, for rows of x without a fixed point.
+__device__ __noinline__ float w4_plain_sum(const W4Params& p, int vec, int m, int n) {
+  const size_t row_bytes = static_cast<size_t>((p.K + p.group - 1) / p.group) * (p.group / 2);
+  const uint4* cr = reinterpret_cast<const uint4*>(p.codes + n * row_bytes);
   float v = 0.f;
-  for (int k = 0; k < p.K; ++k) {
-    const int c = (cr[k >> 1] >> (4 * (k & 1))) & 15;
-    float x = w4_load(p.x, p.x_f32, static_cast<size_t>(m) * p.K + k);
-    if (p.silu) x = w4_silu(x);
-    v += x * (w4_bf16(p.scales[static_cast<size_t>(k / p.group) * p.scale_stride + n]) * (c - 8));
+  for (int k = 0; k < p.K; k += 32) {  // 16 bytes of codes, of one group
+    const uint4 q = cr[k >> 5];
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    const float s = w4_bf16(p.scales[static_cast<size_t>(k / p.group) * p.scale_stride + n]);
+    float part = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float x[8];
+      w4_values(w4_load8(p.x, p.x_f32, vec, static_cast<size_t>(m) * p.K, k + 8 * j, p.K), p.x_f32, x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (p.silu) x[e] = w4_silu(x[e]);
+        part = fmaf(x[e], s * (static_cast<int>((w[j] >> (4 * e)) & 15u) - 8), part);
+      }
+    }
+    v += part;
+  }
+  return v;
+}
+
+// Values of x set aside: how many of each row (W4_FAR + 1 and more: it is summed
+// term by term), their columns and values.
+struct W4Far {
+  int n[W4_MAX_ROWS];
+  int k[W4_MAX_ROWS][W4_FAR];
+  float v[W4_MAX_ROWS][W4_FAR];
+};
+
+// The values of a row in the order of their columns: their order of arrival is
+// not that of the next call, and sums would differ.  A warp a row.
+__device__ __forceinline__ void w4_sort_far(W4Far& F, int m, int lane) {
+  const int n = F.n[m];
+  if (n < 2 || n > W4_FAR) return;
+  const int k = lane < n ? F.k[m][lane] : INT32_MAX;
+  const float v = lane < n ? F.v[m][lane] : 0.f;
+  int rank = 0;
+  for (int i = 0; i < n; ++i) rank += __shfl_sync(0xffffffffu, k, i) < k;
+  __syncwarp();
+  if (lane < n) {
+    F.k[m][rank] = k;
+    F.v[m][rank] = v;
+  }
+}
+
+// What the set-aside values of row m add to row n of the weights.
+__device__ __noinline__ float w4_far_sum(const W4Params& p, const W4Far& F, int m, int n) {
+  const size_t row_bytes = static_cast<size_t>((p.K + p.group - 1) / p.group) * (p.group / 2);
+  const uint8_t* cr = p.codes + n * row_bytes;
+  float v = 0.f;
+  for (int i = 0; i < F.n[m]; ++i) {
+    const int k = F.k[m][i], c = (cr[k >> 1] >> (4 * (k & 1))) & 15;
+    v = fmaf(F.v[m][i], w4_bf16(p.scales[static_cast<size_t>(k / p.group) * p.scale_stride + n]) * (c - 8), v);
   }
   return v;
 }
@@ -387,10 +452,12 @@ struct W4X {
 // into shared memory.  A warp takes a row's chunk, a lane eight columns: of
 // each digit one 8-byte store in the order 0, 2, 4, 6, 1, 3, 5, 7, as a word of
 // codes unpacks.  fac: what the chunk's sums of a digit stand for; off: minus
-// the magic number and 8 sum q of each group.  bad[m] is set if a value is not finite.
+// the magic number and 8 sum q of each group.  Values set aside go to F, in
+// any order.  Returns whether this thread found one, or one that is not finite.
 template <int G, int W, int NT>
-__device__ __forceinline__ void w4_stage_x(const W4Launch& L, int m0, int rows, const W4X& X, int* bad, int k0,
+__device__ __forceinline__ bool w4_stage_x(const W4Launch& L, int m0, int rows, const W4X& X, W4Far& F, int k0,
                                            int chunks) {
+  bool found = false;
   const W4Params& p = L.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int items = rows * chunks;
@@ -409,15 +476,46 @@ __device__ __forceinline__ void w4_stage_x(const W4Launch& L, int m0, int rows, 
     const int m = i / chunks, c = i - m * chunks;
     float v[8], a = 0.f;
     w4_values(raw, p.x_f32, v);
-    bool fine = true;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       if (p.silu) v[e] = w4_silu(v[e]);
-      a = fmaxf(a, fabsf(v[e]));
-      fine &= fabsf(v[e]) < INFINITY;
+      a = w4_max_nan(a, fabsf(v[e]));
     }
-    asm volatile("redux.sync.max.abs.f32 %0, %0, 0xffffffff;" : "+f"(a));
-    if (!fine) bad[m] = 1;
+    float mine = a;
+    asm volatile("redux.sync.max.abs.NaN.f32 %0, %0, 0xffffffff;" : "+f"(a));
+    const bool fine = a < INFINITY;
+    if (!fine && lane == 0) atomicMax(&F.n[m], W4_NOT_FINITE);
+    found |= !fine;
+    // 16 lanes with a value within 2^10 of the largest, or four and half as many as have any, are one in 16 at
+    // least: nothing is set aside.  Else the values are counted; each turn takes some off and the next largest is
+    // 2^10 below, so there are fewer than 30 turns.
+    while (fine) {
+      const float least = a * 0x1p-10f;
+      const int lanes = __popc(__ballot_sync(0xffffffffu, mine >= least));
+      if (lanes >= 16 || (lanes >= 4 && __popc(__ballot_sync(0xffffffffu, mine > 0.f)) <= 2 * lanes)) break;
+      int count = 0;  // values of at least that, and 65536 for each that is not zero
+#pragma unroll
+      for (int e = 0; e < 8; ++e) count += (fabsf(v[e]) >= least ? 1 : 0) + (v[e] != 0.f ? 65536 : 0);
+      count = __reduce_add_sync(0xffffffffu, count);
+      const int near = count & 65535, some = count >> 16;
+      if (some <= near || (near >= 4 && some <= 16 * near)) break;
+      found = true;
+      mine = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (fabsf(v[e]) >= least) {
+          const int at = atomicAdd(&F.n[m], 1);
+          if (at < W4_FAR) {
+            F.k[m][at] = k0 + 8 * (c * 32 + lane) + e;
+            F.v[m][at] = v[e];
+          }
+          v[e] = 0.f;
+        }
+        mine = fmaxf(mine, fabsf(v[e]));
+      }
+      a = mine;
+      asm volatile("redux.sync.max.abs.f32 %0, %0, 0xffffffff;" : "+f"(a));
+    }
     const bool small = a < W4_SMALL;
     if (small) {
       a *= 0x1p24f;
@@ -449,6 +547,7 @@ __device__ __forceinline__ void w4_stage_x(const W4Launch& L, int m0, int rows, 
       if (lane == d) sts_f1(X.fac + (c * (NT * 8) + col) * 4, down * static_cast<float>(1 << (8 * d)));
     }
   }
+  return found;
 }
 
 // N words at a shared-memory address.
@@ -478,7 +577,8 @@ __global__ void __launch_bounds__(32 * w4_warps(NT), 1)
   constexpr int RED = w4_red_rows(NT), RED_LD = w4_red_pitch(NT);
   constexpr int XR = NT * 8 / W4_DIGITS;             // rows of x of the columns
   __shared__ uint64_t full[W][W4_MAX_STAGES];
-  __shared__ int abort_flag, bad[W4_MAX_ROWS];
+  __shared__ int abort_flag;
+  __shared__ W4Far far;
   constexpr int GPC = W4_CHUNK / G;              // groups per chunk
   constexpr int WORDS = G / 32;                  // words of a lane per row and group
   constexpr int SC_STAGE = (ROWS * GPC * 2 + 127) / 128 * 128;  // scale bytes per stage
@@ -495,7 +595,7 @@ __global__ void __launch_bounds__(32 * w4_warps(NT), 1)
   X.x = red_base + W * XR * RED_LD * 4;
   X.fac = X.x + W4_DIGITS * L.rows_m * L.x_pitch;
   X.off = X.fac + L.seg_chunks * NT * 32;
-  if (threadIdx.x < W4_MAX_ROWS) bad[threadIdx.x] = 0;
+  if (threadIdx.x < W4_MAX_ROWS) far.n[threadIdx.x] = 0;
   if (threadIdx.x == 0) abort_flag = 0;
   if (lane == 0) {
     for (int i = 0; i < L.stages; ++i) mbar_init(smem_u32(&full[warp][i]), 1);
@@ -546,10 +646,11 @@ __global__ void __launch_bounds__(32 * w4_warps(NT), 1)
   bool ok = true;
   int st = 0;
   uint32_t ph = 0;
+  int any_far = 0;  // of the whole CTA
   if (L.segs == 1) {
-    __syncthreads();  // bad[] is clear
-    w4_stage_x<G, W, NT>(L, m0, rows, X, bad, 0, L.seg_chunks);
-    __syncthreads();  // (segs > 1: at the first part, before the first wait too)
+    __syncthreads();  // far.n is clear
+    any_far = __syncthreads_or(w4_stage_x<G, W, NT>(L, m0, rows, X, far, 0, L.seg_chunks));
+    // (segs > 1: at the first part, before the first wait too)
   }
   for (int round = 0; round * round_blocks < L.blocks; ++round) {
     const int block = first_block + round * round_blocks;
@@ -562,8 +663,11 @@ __global__ void __launch_bounds__(32 * w4_warps(NT), 1)
     for (int chunk = 0; chunk < L.chunks; chunk += kw_n, xc += kw_n) {
       if (L.segs > 1 && chunk % L.seg_chunks == 0) {  // x does not fit whole: its next part
         __syncthreads();
-        w4_stage_x<G, W, NT>(L, m0, rows, X, bad, chunk * W4_CHUNK, L.seg_chunks);
-        __syncthreads();
+        if (chunk == 0 && any_far) {  // x anew
+          if (threadIdx.x < W4_MAX_ROWS) far.n[threadIdx.x] = 0;
+          __syncthreads();
+        }
+        any_far |= __syncthreads_or(w4_stage_x<G, W, NT>(L, m0, rows, X, far, chunk * W4_CHUNK, L.seg_chunks));
         xc = kw;
       }
       if (block >= L.blocks || chunk + kw >= L.chunks) continue;  // the last round, a last step: nothing for this warp
@@ -638,6 +742,10 @@ __global__ void __launch_bounds__(32 * w4_warps(NT), 1)
         ph ^= 1u;
       }
     }
+    if (any_far && (L.segs > 1 || round == 0)) {
+      if (warp < rows) w4_sort_far(far, warp, lane);
+      __syncthreads();
+    }
     // the round's sums, RED rows of each warp at a time: the neighbouring lanes' halves of a row of x, then
     // over the KW warps
 #pragma unroll
@@ -659,12 +767,13 @@ __global__ void __launch_bounds__(32 * w4_warps(NT), 1)
         const int n = ((round * rw_n + from) * gridDim.x + blockIdx.x) * ROWS + 16 * h0 + r;
         if (n >= p.N || !ok) return;
         float v = 0.f;
-        if (bad[m]) {
-          v = w4_plain_sum(p, m0 + m, n);
+        if (any_far && far.n[m] > W4_FAR) {
+          v = w4_plain_sum(p, L.x_vec, m0 + m, n);
         } else {
           const uint32_t at = red_base + ((from * XR + m) * RED_LD + r) * 4;
           for (int k = 0; k < kw_n && k < L.chunks; ++k)
             v += __uint_as_float(lds32(at + k * rw_n * XR * RED_LD * 4));
+          if (any_far) v += w4_far_sum(p, far, m, n);
         }
         if (p.bias) v += p.bias[n];
         w4_store(p.out, p.out_f32, static_cast<size_t>(m0 + m) * p.out_stride + n, v);
@@ -695,7 +804,7 @@ static cudaError_t linear_w4_launch(const W4Launch& L, const CUtensorMap& tc, co
   cudaGetDevice(&dev);
   if (!((done >> dev) & 1u)) {
     const cudaError_t e =
-        cudaFuncSetAttribute(linear_w4_kernel<NT, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, W4_SMEM_MAX - 2048);
+        cudaFuncSetAttribute(linear_w4_kernel<NT, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, W4_SMEM_MAX - W4_STATIC);
     if (e != cudaSuccess) return e;
     done |= uint64_t(1) << dev;
   }
@@ -727,7 +836,7 @@ cudaError_t launch_linear_w4(const W4Params& whole_p, cudaStream_t s) {
   L.rows_m = (p.M + passes - 1) / passes;
   const int cols = W4_DIGITS * L.rows_m, nt = (cols + 7) / 8, warps = w4_warps(nt), rows = W4_ROWS;
   const int stage = warps * (rows * W4_CHUNK / 2 + rows * (W4_CHUNK / p.group) * 2);
-  const int fixed = warps * nt * 8 / W4_DIGITS * w4_red_pitch(nt) * 4 + 3072;  // sums, alignment, static barriers
+  const int fixed = warps * nt * 8 / W4_DIGITS * w4_red_pitch(nt) * 4 + 1024 + W4_STATIC;  // sums, alignment, static
   // x lies in shared memory whole if two stages fit beside it, else in parts
   // of `seg` chunks, a multiple of the chunks that share a row; columns are
   // spaced so that the lanes of a bank cycle differ
@@ -763,7 +872,7 @@ cudaError_t launch_linear_w4(const W4Params& whole_p, cudaStream_t s) {
   const int x_bytes = cols * pad + L.seg_chunks * chunk_bytes;
   const int left = W4_SMEM_MAX - fixed - x_bytes;
   L.stages = left / stage < W4_MAX_STAGES ? left / stage : W4_MAX_STAGES;
-  const size_t smem = fixed - 2048 + static_cast<size_t>(x_bytes) + static_cast<size_t>(L.stages) * stage;
+  const size_t smem = fixed - W4_STATIC + static_cast<size_t>(x_bytes) + static_cast<size_t>(L.stages) * stage;
   CUtensorMap tc, ts;
   if (!encode_tmap_2d(&tc, p.codes, row_bytes, p.N, row_bytes, W4_CHUNK / 2, rows, true) ||
       !encode_tmap_2d(&ts, p.scales, p.N, groups, static_cast<uint64_t>(p.scale_stride) * 2, rows,

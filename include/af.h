@@ -410,7 +410,8 @@ af_status af_dequantize_rows_w4(const uint8_t* codes, const uint16_t* scales, in
 
 /* out[m, n] = bias[n] + sum_k f(x[m, k]) value(n, k), f = SiLU if silu != 0,
  * else the identity: the adaLN-Zero modulations W silu(temb) ([ARCH]
- * §联合注意力块) and other projections of a few rows.  f(x) enters as 32-bit
+ * §联合注意力块) and other projections of a few rows; SiLU to two fp32 steps
+ * (2^-22), 0 below -88.7.  f(x) enters as 32-bit
  * fixed point with a power of two as its step per row and 256 columns, at most
  * 2^-30 (1 + 2^-7) of the largest magnitude there: magnitudes from 2^-6 of the
  * largest on are exact, others off by at most half a step.

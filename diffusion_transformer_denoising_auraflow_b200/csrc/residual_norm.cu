@@ -8,6 +8,8 @@
 // post, pre: no norm, LayerNorm (biased variance) or RMS norm, each with eps
 // under the root and statistics in fp32 (LayerNorm: the mean first, then the
 // centred squares).  y is formed from x' before it is rounded for storage.
+#include <atomic>
+
 #include "af_internal.h"
 #include "ptx.cuh"
 
@@ -782,7 +784,7 @@ static cudaError_t rn_go(const ResidualNormParams& p, const RnPlan& plan, unsign
                          cudaStream_t s) {
   // The opt-in at every size: what launches without it is 48 KB less the kernel's
   // own arrays (2 KB of sums), which the factors alone reach at 3944 columns.
-  static uint64_t done = 0;  // one bit per device: the kernel's shared-memory opt-in
+  static std::atomic<uint64_t> done{0};  // one bit per device: the kernel's shared-memory opt-in
   int dev = 0;
   cudaGetDevice(&dev);
   if (!((done >> dev) & 1u)) {
@@ -797,8 +799,7 @@ static cudaError_t rn_go(const ResidualNormParams& p, const RnPlan& plan, unsign
 
 template <typename T, bool OUT8>
 static cudaError_t rn_launch(const ResidualNormParams& p, cudaStream_t s) {
-  static int sms = 0;
-  if (!sms) sms = device_sm_count();
+  static const int sms = device_sm_count();
   const int n8 = p.D / 8;
   RnPlan plan;
   int v;
@@ -869,7 +870,7 @@ static cudaError_t rn_launch(const ResidualNormParams& p, cudaStream_t s) {
 
 template <typename T, bool OUT8, int V>
 static cudaError_t rn_shift(const ResidualNormParams& p, const RnPlan& plan, cudaStream_t s) {
-  static uint64_t done = 0;  // one bit per device: the kernel's shared-memory opt-in
+  static std::atomic<uint64_t> done{0};  // one bit per device: the kernel's shared-memory opt-in
   int dev = 0;
   cudaGetDevice(&dev);
   if (!((done >> dev) & 1u)) {
@@ -886,8 +887,7 @@ static cudaError_t rn_shift(const ResidualNormParams& p, const RnPlan& plan, cud
 template <typename T, bool OUT8>
 static cudaError_t rn_any(const ResidualNormParams& p, bool aligned, cudaStream_t s) {
   const size_t rows = static_cast<size_t>(p.B) * p.rows_per_batch;
-  static int sms = 0;
-  if (!sms) sms = device_sm_count();
+  static const int sms = device_sm_count();
   // enough rows for every SM to take more than a round of them: aligned vectors
   // of each row.  1001 columns, value by value against this (us): 1 row 3.1 and
   // 5.5, 500 rows 4.0 and 7.1, 1200 rows 6.1 and 7.5, 2400 rows 11.2 and 12.3; 6000

@@ -7,6 +7,8 @@
 // k of row n in the low (k even) or high (k odd) nibble of byte k / 2, code 8
 // (the value zero) behind column K; scales bf16 [ceil(K / G), scale_stride],
 // group-major so the scales of neighbouring rows are neighbours.
+#include <atomic>
+
 #include "af_internal.h"
 #include "ptx.cuh"
 
@@ -806,7 +808,7 @@ __global__ void __launch_bounds__(32 * w4_warps(NT), 1)
 template <int NT, int G>
 static cudaError_t linear_w4_launch(const W4Launch& L, const CUtensorMap& tc, const CUtensorMap& ts, size_t smem,
                                     dim3 grid, cudaStream_t s) {
-  static uint64_t done = 0;  // one bit per device: the kernel's shared-memory opt-in
+  static std::atomic<uint64_t> done{0};  // one bit per device: the kernel's shared-memory opt-in
   int dev = 0;
   cudaGetDevice(&dev);
   if (!((done >> dev) & 1u)) {
@@ -831,8 +833,7 @@ cudaError_t launch_linear_w4(const W4Params& whole_p, cudaStream_t s) {
     p = whole_p;
     p.M = MOST;
   }
-  static int sms = 0;
-  if (!sms) sms = device_sm_count();
+  static const int sms = device_sm_count();
   const int groups = (p.K + p.group - 1) / p.group;
   const int row_bytes = groups * (p.group / 2);
   W4Launch L;

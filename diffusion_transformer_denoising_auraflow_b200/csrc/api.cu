@@ -1094,11 +1094,22 @@ af_status af_weights_quantize_fp8(af_weights* w, int enable, void* stream) {
   return AF_OK;
 }
 
+// Whether work on the stream is being captured, where memory is neither
+// allocated nor freed; true where that cannot be told.
+static bool capturing(void* stream) {
+  cudaStreamCaptureStatus c = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &c) == cudaSuccess)
+    return c != cudaStreamCaptureStatusNone;
+  cudaGetLastError();
+  return true;
+}
+
 af_status af_weights_quantize_w4(af_weights* w, int group, void* stream) {
   if (!w) return AF_ERR_INVALID_ARG;
   if (!(group == 0 || group == 32 || group == 64 || group == 128)) return AF_ERR_UNSUPPORTED;
   AF_TRY(check_device(w));
   if (group != w->w4_group) {
+    if (capturing(stream)) return AF_ERR_UNSUPPORTED;
     if (w->w4_codes) cudaFree(w->w4_codes);
     if (w->w4_scales) cudaFree(w->w4_scales);
     w->w4_codes = nullptr;

@@ -438,7 +438,10 @@ af_status af_linear_w4(const void* x, int x_dtype, int silu, const uint8_t* code
  * pack's own weights.  The quantiser runs on `stream`: work on `w` on other
  * streams waits for it or has ended.  When the copy is freed or re-made with
  * another group, work on `w` in flight must have ended, and graphs captured
- * from calls on `w` since it was made are not replayed any more. */
+ * from calls on `w` since it was made are not replayed any more.  Both
+ * allocate or free memory: on a stream that is being captured that is
+ * AF_ERR_UNSUPPORTED, and only the same group again is recorded.  After
+ * AF_ERR_OOM the pack computes from its own weights. */
 af_status af_weights_quantize_w4(af_weights* w, int group, void* stream);
 
 /* Host-side sigma schedule of the flow-match Euler sampler ([DEEP] §2.3:

@@ -33,6 +33,11 @@ __device__ __forceinline__ void rn_store(void* p, size_t i, float v) {
 // value.  Up to 128 columns TG is a power of two within a warp, the columns TG
 // apart, and a CTA takes 256 / TG rows; wider rows take whole warps, each E times
 // 32 neighbouring columns (constant offsets), and above a warp a CTA each.
+// Bound: the loads and stores of single values (two 4360 x 3072 bf16 samples off
+// 16-byte boundaries 103 us, 42 on them).  With 16 columns a thread, rows above
+// 8192 columns, registers do not hold them all: 340 to 948 bytes a thread go to
+// local memory; 2400 rows of 9001 columns take 82 us in bf16 and 135 in fp32,
+// where HBM would allow 26 and 53.
 constexpr int RN_THREADS = 256;
 
 template <typename T, bool OUT8, int E, bool WIDE>
@@ -163,6 +168,8 @@ __global__ void __launch_bounds__(1024)
 // group in shared memory, bulk copies issued by its first thread as soon as
 // the group has a row in registers; at 3072 columns seven groups keep two rows
 // each, 168 KB, in flight.
+// Registers: bf16 fits up to 16 bytes a thread in local memory (the ring, 80 of
+// them); fp32 at three and four vectors has 104 to 220 bytes there.
 // Statistics are two-pass; sums are joined by shuffles and, for rows wider
 // than a warp, through shared memory at the row group's named barrier, two
 // buffers in turn so that one barrier per sum is enough.  Packed fp32 pairs.
@@ -580,6 +587,9 @@ __global__ void __launch_bounds__(RING ? RN_RING_THREADS : 512, V == 1 ? 2 : 1)
 // rows: they are read with the rest, taken as zero, and not written.  Factors
 // lie in shared memory in eight planes by column mod 8, where the lanes' columns
 // 8 apart are neighbours whatever off is.
+// Bound: instructions, the 24 factors of a vector read one by one and the masks:
+// two 4360 x 3001 bf16 samples 57 us (32 at HBM's rate).  In fp32 four vectors a
+// thread do not fit the registers: 684 to 804 bytes go to local memory.
 template <typename T, bool OUT8, int V>
 __global__ void __launch_bounds__(512, 1)
     residual_norm_shift_kernel(const __grid_constant__ ResidualNormParams p, const RnPlan plan) {

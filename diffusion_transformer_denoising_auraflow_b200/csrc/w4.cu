@@ -304,7 +304,7 @@ cudaError_t launch_dequantize_rows_w4(const uint8_t* codes, const uint16_t* scal
 // Other operands cost more to make: c - 8 in fp16 (x in two pieces) took 77
 // instructions per 16 rows and 64 columns against 45, near the 91 issue slots
 // that HBM leaves time for; 743424 x 3072 with two rows of x took 218 us
-// against 193 (6.3 TB/s).
+// against 198 (6.1 TB/s).
 // One step does not fit 256 columns of which most are far below the largest:
 // the others' last bits show in weights that are zero at the few large ones.
 // Where fewer than four, or than one in 16, of the values other than zero reach
@@ -331,8 +331,8 @@ cudaError_t launch_dequantize_rows_w4(const uint8_t* codes, const uint16_t* scal
 // smaller rings leave shared memory for it.  With three columns a row of x,
 // sixteen warps of 16 rows against twelve of 32: 743424 x 3072 with eight rows of
 // x 305 us and 298, 55296 x 3072 with twenty 65 and 62.  Four columns against
-// three, 120000 x 3072 with 2, 4, 8, 10 and 32 rows: 38, 49, 75, 99 and 238 us against
-// 38, 50, 63, 165 (x in parts) and 185.
+// three, 120000 x 3072 with 1, 4, 8, 10 and 32 rows: 37, 49, 74, 101 and 231 us
+// against 38, 50, 63, 165 (x in parts) and 185.
 __host__ __device__ constexpr int w4_warps(int nt) { return nt == 1 ? 16 : 12; }
 constexpr int W4_ROWS = 32;                               // rows per warp
 // Rows of a warp whose sums are joined through shared memory at a time, and the
@@ -855,9 +855,9 @@ cudaError_t launch_linear_w4(const W4Params& whole_p, cudaStream_t s) {
   const int per = passes < sms ? sms / passes : 1;  // CTAs per part of x's rows
   // the split with the least time on the busiest SM: rounds of row blocks, each
   // a chunk time per step, the round's bytes and a fixed end.  Against one warp
-  // per row block (KW = 1): 18432 x 3072, two rows of x, 11.5 us and 18.6;
-  // 3072 x 3072, one row, 4.9 and 16.6; 4099 x 2051, seven rows, 10.8 and 25.5; with
-  // 743424 rows of weights both 199.
+  // per row block (KW = 1): 18432 x 3072, two rows of x, 11.7 us and 18.5;
+  // 3072 x 3072, one row, 4.8 and 16.3; 4099 x 2051, seven rows, 11.7 and 30.1; with
+  // 743424 rows of weights both 198; with 120000 it is off by a little, 39.0 and 36.6.
   L.blocks = (p.N + rows - 1) / rows;
   float best = 0.f;
   L.rw = 0;

@@ -150,3 +150,17 @@ def test_the_bound_shows_a_lost_byte():
         ref = _plain(x, w)
         err = (_plain(torch.round(x / step) * step, w) - ref).abs()
         assert torch.any(err > _bound(x, w, K, 128, ref))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_more_rows_than_one_launch_takes(af, dtype):
+    """65535 CTAs of eight rows of x, and some rows behind them."""
+    g = torch.Generator(device="cuda").manual_seed(875)
+    M, N, K = 8 * 65535 + 13, 3, 33
+    x = torch.randint(-100, 101, (M, K), device="cuda", generator=g).to(dtype)
+    c = torch.randint(0, 16, (N, K), device="cuda", generator=g)
+    scales = torch.ones(2, 8, dtype=BF, device="cuda")
+    out = torch.full((M + 1, N), 3.0, device="cuda")
+    af.linear_w4(x, _pack(c, 32), scales, 32, out[:M])
+    assert torch.equal(out[:M].double(), _plain(x, _values(c, scales, 32)))   # whole numbers below 2^24
+    assert torch.all(out[M] == 3.0)

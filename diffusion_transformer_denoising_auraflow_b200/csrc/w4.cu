@@ -302,7 +302,7 @@ cudaError_t launch_dequantize_rows_w4(const uint8_t* codes, const uint16_t* scal
 // 8 sum q known per group and column, then multiplied by the group's scale and
 // added up in fp32.
 // Other operands cost more to make: c - 8 in fp16 (x in two pieces) took 77
-// instructions per 16 rows and 64 columns against 45, near the 91 issue slots
+// instructions per 16 rows and 64 columns against 46, near the 91 issue slots
 // that HBM leaves time for; 743424 x 3072 with two rows of x took 218 us
 // against 198 (6.1 TB/s).
 // One step does not fit 256 columns of which most are far below the largest:
@@ -311,9 +311,9 @@ cudaError_t launch_dequantize_rows_w4(const uint8_t* codes, const uint16_t* scal
 // 2^-10 of the largest, these are set aside (W4_FAR a row at most, in the order of
 // their columns) and added as fp32 terms of their own to the finished sums; the
 // step is that of the rest.  A row with more of them, an infinity or a NaN is
-// summed term by term in fp32 (w4_plain_sum).  18432 x 3072 with a value set aside in each of one row
-// and of seven: 10.3 us and 24 against 9.2 and 18.5; one row and seven summed term by
-// term 143 and 634.
+// summed term by term in fp32 (w4_plain_sum).  18432 x 3072 with a value set
+// aside in one row of x and in each of seven: 10.3 us and 24 against 9.2 and 18.5;
+// one row and seven summed term by term 143 and 634.
 //
 // Bound: the code bytes from HBM (4.25 bits a weight at G = 64).  One CTA of W
 // warps per SM, RW x KW of them: RW blocks of 32 rows by KW ways to
@@ -359,9 +359,9 @@ struct W4Launch {
 // Fixed point: a (1 + 2^-7) < 2^(e + 1) counts in steps of 2^(e - 30), so that
 // a's number is below 2^31 / (1 + 2^-7) = 2130836295; four signed bytes reach
 // 2139062143.  e is kept so that the step is no smaller than fp32's smallest, 2^-149.
-constexpr int W4_FAR = 32;                                // values set aside a row, a warp's lanes
-constexpr int W4_NOT_FINITE = 1 << 30;                    // their count where the row has an infinity or NaN
 constexpr float W4_SMALL = 0x1p-90f;       // where the largest is below this, scaled by 2^24 first
+constexpr int W4_FAR = 32;                 // values set aside a row: a warp's lanes
+constexpr int W4_NOT_FINITE = 1 << 30;     // their count where the row has an infinity or NaN
 constexpr int W4_MAGIC_BITS = 0x4B400000;
 
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
@@ -422,6 +422,7 @@ struct W4Far {
   int k[W4_MAX_ROWS][W4_FAR];
   float v[W4_MAX_ROWS][W4_FAR];
 };
+static_assert(sizeof(W4Far) + 16 * W4_MAX_STAGES * 8 + 64 <= W4_STATIC, "the kernel's own shared memory");
 
 // The values of a row in the order of their columns: their order of arrival is
 // not that of the next call, and sums would differ.  A warp a row.
